@@ -3,8 +3,10 @@
 libasyncpipe streams float32 tiles from global to shared memory through an
 mbarrier-tracked ring of asynchronous bulk copies on GB300 (sm_103a) and
 computes on them: scale, row shift, Horner polynomial, and a CTA-to-CTA
-shared-memory hand-off inside a thread-block cluster. The C interface is
-declared in ``include/asyncpipe.h``; these functions carry the same names and
+shared-memory hand-off inside a thread-block cluster; and the operators of a
+layer in 8-bit floating point (norm, its gradient, quantiser, matrix product).
+The C interface is declared in ``include/asyncpipe.h`` and
+``include/asyncpipe_fp8.h``; these functions carry the same names and
 arguments and only marshal them. PyTorch provides device memory and streams.
 """
 
@@ -20,6 +22,11 @@ __all__ = [
     "ap_cluster_exchange_ex",
     "ap_cluster_all_to_all",
     "ap_masked_copy",
+    "ap_rms_norm",
+    "ap_rms_norm_backward",
+    "ap_rms_norm_backward_workspace",
+    "ap_quantize",
+    "ap_matmul_fp8",
     "ap_autotune",
     "ap_autotune_reset",
     "ap_check",

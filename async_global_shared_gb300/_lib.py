@@ -3,8 +3,10 @@
 Every function has the C entry point's name and arguments. Buffers may be
 given as torch tensors (float32, on the current CUDA device, contiguous) or as
 raw integer device addresses; ``stream`` may be a ``torch.cuda.Stream``, a raw
-``cudaStream_t`` integer, or None for torch's current stream. A status other
-than AP_OK raises :class:`APError`. Nothing here computes: every step runs in
+``cudaStream_t`` integer, or None for torch's current stream. The 8-bit
+block-scaled operators (``ap_rms_norm`` and those after it) take torch tensors
+only: their shapes, types and row strides fill in the C call's sizes, element
+types and leading dimensions. A status other than AP_OK raises :class:`APError`. Nothing here computes: every step runs in
 the library's CUDA kernels, and a missing library raises instead of falling
 back to anything else.
 """
@@ -89,12 +91,22 @@ EXPORTED = (
     "ap_debug_fma_probe",
     "ap_debug_fma_probe_horner",
     "ap_debug_scale_pages_async",
+    "ap_rms_norm",
+    "ap_rms_norm_backward",
+    "ap_rms_norm_backward_workspace",
+    "ap_quantize",
+    "ap_matmul_fp8",
 )
 
 
 AP_TUNE_SCALE = 1
 AP_TUNE_ROW_ROLL = 2
 AP_TUNE_POLY = 3
+
+# ap_dtype
+AP_F32 = 0
+AP_BF16 = 1
+AP_F16 = 2
 
 
 class RingShape(ctypes.Structure):
@@ -146,7 +158,15 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.ap_debug_fma_probe_horner.argtypes = [vp, _i64, _i64, vp]
     lib.ap_debug_scale_pages_async.argtypes = [vp, vp, _i64, _i64, ctypes.c_float, vp]
     lib.ap_debug_emulate_ring_tensor.argtypes = [vp, vp, _i64, _i64, _i64, _i64, _i64]
-    for name in ("ap_scale", "ap_scale_sync", "ap_row_roll", "ap_poly", "ap_cluster_exchange",
+    f32, i32 = ctypes.c_float, ctypes.c_int
+    lib.ap_rms_norm.argtypes = [vp, _i64, i32, vp, vp, _i64, i32, vp, i32, f32, _i64, _i64, vp, _i64, vp, _i64, vp, vp, vp]
+    lib.ap_rms_norm_backward.argtypes = [vp, _i64, i32, vp, _i64, i32, vp, i32, vp, vp, _i64, _i64, _i64, vp, _i64, vp,
+                                         vp, vp]
+    lib.ap_rms_norm_backward_workspace.argtypes = [_i64, _i64]
+    lib.ap_rms_norm_backward_workspace.restype = _i64
+    lib.ap_quantize.argtypes = [vp, _i64, i32, _i64, _i64, i32, vp, _i64, vp, vp, _i64, vp, vp]
+    lib.ap_matmul_fp8.argtypes = [vp, _i64, vp, vp, _i64, vp, i32, vp, _i64, i32, _i64, _i64, _i64, vp]
+    for name in ("ap_rms_norm", "ap_rms_norm_backward", "ap_quantize", "ap_matmul_fp8", "ap_scale", "ap_scale_sync", "ap_row_roll", "ap_poly", "ap_cluster_exchange",
                  "ap_cluster_exchange_ex", "ap_cluster_all_to_all", "ap_masked_copy", "ap_autotune", "ap_autotune_reset", "ap_check",
                  "ap_debug_set", "ap_debug_emulate_ring", "ap_debug_emulate_ring_tensor", "ap_debug_fma_probe",
                  "ap_debug_fma_probe_horner", "ap_debug_scale_pages_async"):
@@ -324,3 +344,190 @@ def ap_debug_fma_probe_horner(out, out_elems: int, iters: int, stream=None):
 def ap_debug_scale_pages_async(inp, out, n_tiles: int, tile_elems: int, alpha: float, stream=None):
     _check(load().ap_debug_scale_pages_async(_addr(inp), _addr(out), n_tiles, tile_elems, alpha, _stream(stream)),
            "ap_debug_scale_pages_async")
+
+
+# ------------------------------------------------------------------ 8-bit block-scaled operators
+
+SCALE_BLOCK = 128  # values of a row that share a scale
+
+
+def _blocks(n: int) -> int:
+    return -(-n // SCALE_BLOCK)
+
+
+_DTYPES = None  # torch dtype -> ap_dtype, and the dtypes that hold e4m3 codes
+
+
+def _dtypes():
+    global _DTYPES
+    if _DTYPES is None:
+        import torch
+
+        _DTYPES = ({torch.float32: AP_F32, torch.bfloat16: AP_BF16, torch.float16: AP_F16},
+                   (torch.float8_e4m3fn, torch.uint8), torch._C._cuda_getDevice)
+    return _DTYPES
+
+
+def _on_device(t, name: str):
+    if not t.is_cuda or t.get_device() != _dtypes()[2]():
+        raise TypeError(f"{name} must be a tensor on the current CUDA device")
+
+
+def _kind(t, name: str) -> int:
+    kind = _dtypes()[0].get(t.dtype)
+    if kind is None:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
+    return kind
+
+
+def _matrix(t, name: str, shape=None) -> int:
+    """Leading dimension of a 2-D tensor with unit column stride, on the current device."""
+    _on_device(t, name)
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{name} must be a matrix{'' if shape is None else ' of shape %s' % (tuple(shape),)}, got {tuple(t.shape)}")
+    rows, cols = t.shape
+    row_stride, col_stride = t.stride()
+    if cols > 1 and col_stride != 1:
+        raise ValueError(f"{name} must have a column stride of 1")
+    if rows <= 1:
+        # a single row's stride is never used: give one its columns fit in and
+        # that the 16-byte rule of the products accepts
+        return -(-cols // 16) * 16
+    if row_stride < cols:
+        raise ValueError(f"{name} must have rows that do not overlap")
+    return row_stride
+
+
+def _codes(t, name: str, shape) -> int:
+    if t.dtype not in _dtypes()[1]:
+        raise TypeError(f"{name} must be float8_e4m3fn (or uint8 codes), got {t.dtype}")
+    return _matrix(t, name, shape)
+
+
+def _floats(t, name: str, shape):
+    """Address of a contiguous float32 tensor of this shape."""
+    import torch
+
+    _on_device(t, name)
+    if t.dtype != torch.float32 or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be a contiguous float32 tensor of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _weight(t, cols: int) -> int:
+    _on_device(t, "weight")
+    if tuple(t.shape) != (cols,) or not t.is_contiguous():
+        raise ValueError(f"weight must be a contiguous vector of {cols}, got {tuple(t.shape)}")
+    return _kind(t, "weight")
+
+
+def ap_rms_norm(x, weight, eps: float, y=None, q=None, q_scales=None, residual=None, residual_out=None, rstd=None,
+                stream=None):
+    """h = x + residual; r = 1 / sqrt(mean(h^2) + eps); y = h * r * weight over each row of x (rows x cols).
+
+    ``y``: the output in x's type; ``q`` (float8_e4m3fn or uint8) and ``q_scales`` (float32, rows x ceil(cols / 128)):
+    the output in 8 bits. ``residual`` and ``residual_out`` (the same tensor for in place) are of x's type or float32
+    and share a row stride; ``rstd`` receives r, which the gradient needs."""
+    ldx = _matrix(x, "x")
+    shape = x.shape
+    rows, cols = shape
+    ldr = ldy = ldq = cols
+    rtype = kind = _kind(x, "x")
+    if residual is not None:
+        ldr = _matrix(residual, "residual", shape)
+        rtype = _kind(residual, "residual")
+        if residual_out is None:
+            raise ValueError("residual needs residual_out (the same tensor for in place)")
+    if residual_out is not None:
+        if residual is None or residual_out.dtype != residual.dtype or _matrix(residual_out, "residual_out", shape) != ldr:
+            raise ValueError("residual_out must match residual in type and row stride")
+    if y is not None:
+        ldy = _matrix(y, "y", shape)
+        if y.dtype != x.dtype:
+            raise TypeError("y must have x's type")
+    if q is not None:
+        ldq = _codes(q, "q", shape)
+        if q_scales is None:
+            raise ValueError("q needs q_scales")
+    _check(load().ap_rms_norm(
+        x.data_ptr(), ldx, kind, None if residual is None else residual.data_ptr(),
+        None if residual_out is None else residual_out.data_ptr(), ldr, rtype, weight.data_ptr(), _weight(weight, cols),
+        eps, rows, cols, None if y is None else y.data_ptr(), ldy, None if q is None else q.data_ptr(), ldq,
+        None if q_scales is None else _floats(q_scales, "q_scales", (rows, _blocks(cols))),
+        None if rstd is None else _floats(rstd, "rstd", (rows,)), _stream(stream)), "ap_rms_norm")
+
+
+def ap_rms_norm_backward_workspace(rows: int, cols: int) -> int:
+    """Bytes of workspace ap_rms_norm_backward needs for these sizes."""
+    size = load().ap_rms_norm_backward_workspace(rows, cols)
+    if size < 0:
+        raise APError(2, "ap_rms_norm_backward_workspace")
+    return size
+
+
+def ap_rms_norm_backward(dy, h, weight, rstd, dx, dweight=None, workspace=None, dresidual=None, stream=None):
+    """Gradient of ap_rms_norm: ``dx`` (of h's type, the gradient of x and of residual) and ``dweight`` (float32).
+
+    ``h``: the forward call's residual_out, or its x where there was no residual; ``dresidual``: a gradient of h from
+    elsewhere, added to dx; ``workspace``: a contiguous uint8 tensor of at least ap_rms_norm_backward_workspace(rows,
+    cols) bytes, needed with dweight."""
+    lddy = _matrix(dy, "dy")
+    shape = dy.shape
+    rows, cols = shape
+    ldh, lddx = _matrix(h, "h", shape), _matrix(dx, "dx", shape)
+    lddr = cols
+    if dx.dtype != h.dtype:
+        raise TypeError("dx must have h's type")
+    if dresidual is not None:
+        lddr = _matrix(dresidual, "dresidual", shape)
+        if dresidual.dtype != h.dtype:
+            raise TypeError("dresidual must have h's type")
+    if workspace is not None:
+        _on_device(workspace, "workspace")
+        have = workspace.numel() * workspace.element_size()
+        if not workspace.is_contiguous() or (dweight is not None and have < ap_rms_norm_backward_workspace(rows, cols)):
+            raise ValueError(f"workspace must be contiguous, of at least {ap_rms_norm_backward_workspace(rows, cols)} bytes")
+    _check(load().ap_rms_norm_backward(
+        dy.data_ptr(), lddy, _kind(dy, "dy"), h.data_ptr(), ldh, _kind(h, "h"), weight.data_ptr(), _weight(weight, cols),
+        _floats(rstd, "rstd", (rows,)), None if dresidual is None else dresidual.data_ptr(), lddr, rows, cols,
+        dx.data_ptr(), lddx, None if dweight is None else _floats(dweight, "dweight", (cols,)),
+        None if workspace is None else workspace.data_ptr(), _stream(stream)), "ap_rms_norm_backward")
+
+
+def ap_quantize(x, block_rows: int, q=None, scales=None, qt=None, scales_t=None, stream=None):
+    """e4m3 codes and scales of x (rows x cols): ``q`` and ``scales`` as it stands, ``qt`` and ``scales_t`` transposed.
+
+    ``block_rows`` 1: a scale for 128 consecutive values of a row of the output (scales rows x ceil(cols / 128),
+    scales_t cols x ceil(rows / 128)); 128: a scale for each 128 x 128 tile."""
+    ldx = _matrix(x, "x")
+    rows, cols = x.shape
+    ldq, ldqt = cols, rows
+    tile = block_rows if block_rows in (1, SCALE_BLOCK) else 1  # other values are the library's to refuse
+    if q is not None:
+        ldq = _codes(q, "q", (rows, cols))
+        if scales is None:
+            raise ValueError("q needs scales")
+    if qt is not None:
+        ldqt = _codes(qt, "qt", (cols, rows))
+        if scales_t is None:
+            raise ValueError("qt needs scales_t")
+    _check(load().ap_quantize(
+        x.data_ptr(), ldx, _kind(x, "x"), rows, cols, block_rows, None if q is None else q.data_ptr(), ldq,
+        None if scales is None else _floats(scales, "scales", (-(-rows // tile), _blocks(cols))),
+        None if qt is None else qt.data_ptr(), ldqt,
+        None if scales_t is None else _floats(scales_t, "scales_t", (-(-cols // tile), _blocks(rows))),
+        _stream(stream)), "ap_quantize")
+
+
+def ap_matmul_fp8(a, a_scales, b, b_scales, c, b_block_rows: int = SCALE_BLOCK, stream=None):
+    """c = a * b^T of e4m3 matrices: a (m x k) scaled by row blocks, b (n x k) by 128 x 128 tiles (``b_block_rows`` 128)
+    or by row blocks (1), c (m x n) float32, bfloat16 or float16. Rows of a and b start on 16-byte boundaries."""
+    lda, ldb, ldc = _codes(a, "a", a.shape), _codes(b, "b", b.shape), _matrix(c, "c")
+    (m, k), (n, kb) = a.shape, b.shape
+    if k != kb or tuple(c.shape) != (m, n):
+        raise ValueError(f"shapes do not match: a {tuple(a.shape)}, b {tuple(b.shape)}, c {tuple(c.shape)}")
+    tile = b_block_rows if b_block_rows in (1, SCALE_BLOCK) else 1
+    _check(load().ap_matmul_fp8(
+        a.data_ptr(), lda, _floats(a_scales, "a_scales", (m, _blocks(k))), b.data_ptr(), ldb,
+        _floats(b_scales, "b_scales", (-(-n // tile), _blocks(k))), b_block_rows, c.data_ptr(), ldc, _kind(c, "c"),
+        m, n, k, _stream(stream)), "ap_matmul_fp8")

@@ -78,6 +78,26 @@ bool g_dev_ready[kMaxDevices];
 DeviceInfo g_dev[kMaxDevices];
 ap_status g_dev_err[kMaxDevices];
 
+// ------------------------------------------------------------------ validation
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
+
+// Byte ranges [a, a+na) and [b, b+nb) overlap.
+bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + static_cast<uintptr_t>(nb) && y < x + static_cast<uintptr_t>(na);
+}
+
+constexpr int64_t kMaxElems = int64_t(1) << 40;  // keeps every byte offset far from overflow
+
+bool valid_stages(int stages) { return stages >= AP_MIN_STAGES && stages <= AP_MAX_STAGES; }
+
+bool aligned16(const void* a, const void* b) {
+    return ((reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b)) & 15) == 0;
+}
+
+}  // namespace
+
 ap_status current_device(DeviceInfo* out) {
     int dev = -1;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return AP_ERR_CUDA;
@@ -110,26 +130,6 @@ ap_status current_device(DeviceInfo* out) {
     *out = g_dev[dev];
     return g_dev_err[dev];
 }
-
-// ------------------------------------------------------------------ validation
-
-bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
-
-// Byte ranges [a, a+na) and [b, b+nb) overlap.
-bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + static_cast<uintptr_t>(nb) && y < x + static_cast<uintptr_t>(na);
-}
-
-constexpr int64_t kMaxElems = int64_t(1) << 40;  // keeps every byte offset far from overflow
-
-bool valid_stages(int stages) { return stages >= AP_MIN_STAGES && stages <= AP_MAX_STAGES; }
-
-bool aligned16(const void* a, const void* b) {
-    return ((reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b)) & 15) == 0;
-}
-
-}  // namespace
 
 // cuTensorMapEncodeTiled, looked up once through the runtime (no -lcuda).
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {

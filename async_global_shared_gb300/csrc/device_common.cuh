@@ -27,6 +27,11 @@ enum WaitSite : uint32_t {
     SITE_CHECK_PRODUCER = 10,
     SITE_CHECK_CONSUMER = 11,
     SITE_EX_PUSHER_CREDIT = 12,
+    SITE_MM_PRODUCER_EMPTY = 13,
+    SITE_MM_MMA_FULL = 14,
+    SITE_MM_MMA_ACC = 15,
+    SITE_MM_CONSUMER_ACC = 16,
+    SITE_MM_DRAIN = 17,
 };
 
 constexpr uint32_t kStatusTimeout = 9;  // AP_ERR_DEVICE_TIMEOUT

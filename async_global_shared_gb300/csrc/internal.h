@@ -10,6 +10,7 @@
 
 #include "asyncpipe.h"
 #include "asyncpipe_debug.h"
+#include "asyncpipe_fp8.h"
 #include "stream_plan.h"
 
 namespace ap {
@@ -21,6 +22,10 @@ struct DeviceInfo {
     int smem_optin;          // max dynamic shared memory per CTA (opt-in), bytes
     uint32_t* status;        // device address of this device's status word
 };
+
+// The current device's facts; AP_ERR_UNSUPPORTED_DEVICE where it is not
+// compute capability 10.3.
+ap_status current_device(DeviceInfo* out);
 
 // Snapshot of the process-wide tuning / fault-injection settings.
 struct Options {
@@ -61,7 +66,11 @@ enum Path : int64_t {
     PATH_SYNC = 3,
     PATH_EXCHANGE = 4,
     PATH_MASKED = 5,
-    PATH_PAGES_ASYNC = 6
+    PATH_PAGES_ASYNC = 6,
+    PATH_NORM = 7,
+    PATH_NORM_GRAD = 8,
+    PATH_QUANTIZE = 9,
+    PATH_MATMUL = 10
 };
 
 // Arguments of the per-element compute of a ring call.
@@ -130,6 +139,64 @@ ap_status launch_fma_probe_horner(const DeviceInfo& di, float* out, int64_t out_
 // chunk (chunk_bytes / cs bytes each) to rank j (shift unused).
 ap_status launch_exchange(const DeviceInfo& di, const Options& o, const float* in, float* out, int64_t groups, int cs,
                           int64_t chunk_bytes, int64_t shift, bool a2a, cudaStream_t stream);
+
+// Arguments of the 8-bit block-scaled operators as the entry points
+// (fp8_api.cu) have checked them; byte-sized pointers where the element type
+// is a run-time choice.
+struct NormArgs {
+    const void* x;
+    const void* residual;
+    void* residual_out;
+    const void* weight;
+    void* y;
+    uint8_t* q;
+    float* q_scales;
+    float* rstd;
+    int64_t rows, cols, ldx, ldr, ldy, ldq;
+    ap_dtype type, residual_type, weight_type;
+    float eps;
+};
+ap_status launch_rms_norm(const DeviceInfo& di, const NormArgs& a, cudaStream_t stream);
+
+struct NormGradArgs {
+    const void* dy;
+    const void* h;
+    const void* weight;
+    const float* rstd;
+    const void* dresidual;
+    void* dx;
+    float* dweight;
+    float* workspace;
+    int64_t rows, cols, lddy, ldh, lddr, lddx;
+    ap_dtype type, residual_type, weight_type;
+};
+ap_status launch_rms_norm_backward(const DeviceInfo& di, const NormGradArgs& a, cudaStream_t stream);
+// Rows of partial sums (cols floats each) the launcher above writes.
+int64_t norm_grad_partials(int64_t rows, int64_t cols);
+
+struct QuantArgs {
+    const void* x;
+    uint8_t* q;
+    float* scales;
+    uint8_t* qt;
+    float* scales_t;
+    int64_t rows, cols, ldx, ldq, ldqt;
+    ap_dtype type;
+    int block_rows;
+};
+ap_status launch_quantize(const DeviceInfo& di, const QuantArgs& a, cudaStream_t stream);
+
+struct MatmulArgs {
+    const uint8_t* a;
+    const uint8_t* b;
+    const float* a_scales;
+    const float* b_scales;
+    void* c;
+    int64_t m, n, k, lda, ldb, ldc;
+    ap_dtype c_type;
+    int b_block_rows;
+};
+ap_status launch_matmul_fp8(const DeviceInfo& di, const Options& o, const MatmulArgs& a, cudaStream_t stream);
 
 // Largest chunk accepted by ap_cluster_exchange for this much shared memory.
 constexpr int64_t kSmemOptinGB300 = 232448;  // 227 KiB per CTA on compute capability 10.x

@@ -48,7 +48,8 @@ typedef enum ap_debug_key {
                                    in AP_DBG_LAST_SITE) and nothing out of range is accessed */
     /* read-only: what the last call on this process launched */
     AP_DBG_LAST_PATH = 100,     /* 1 ring, 2 small row shift, 3 synchronous, 4 cluster exchange,
-                                   5 masked copy, 6 the pages' asynchronous tiled scale */
+                                   5 masked copy, 6 the pages' asynchronous tiled scale, 7 norm,
+                                   8 norm gradient, 9 quantiser, 10 8-bit matrix product */
     AP_DBG_LAST_GRID = 101,     /* CTAs launched */
     AP_DBG_LAST_STAGE_ELEMS = 102, /* elements per ring stage (chunk elements for exchange) */
     AP_DBG_LAST_SMEM = 103,     /* dynamic shared memory per CTA, bytes */
