@@ -32,6 +32,8 @@ enum WaitSite : uint32_t {
     SITE_MM_MMA_ACC = 15,
     SITE_MM_CONSUMER_ACC = 16,
     SITE_MM_DRAIN = 17,
+    SITE_MM_SCALES_EMPTY = 18,
+    SITE_MM_SCALES_FULL = 19,
 };
 
 constexpr uint32_t kStatusTimeout = 9;  // AP_ERR_DEVICE_TIMEOUT

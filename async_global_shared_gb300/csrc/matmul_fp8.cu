@@ -2,16 +2,30 @@
 //     c[i, j] = sum over blocks kb of sa[i, kb] sb[j, kb] * P_kb[i, j],
 //     P_kb[i, j] = sum over the block's 128 k of a[i, k] b[j, k].
 // The scales differ from row to row and from block to block, so P_kb cannot
-// stay in the tensor core's accumulator: each block's products go to their own
-// accumulator in tensor memory, and consumer threads read it, multiply it by
-// the two scales and add it to sums in registers while the tensor core works
-// on the next block.
+// stay in the tensor core's accumulator: each block's products go to an
+// accumulator of their own in tensor memory, and consumer threads read it,
+// multiply it by the two scales and add it to sums in registers while the
+// tensor core works on the next blocks.
 //
-// One CTA computes a 128 x 128 tile. A producer thread streams the operands'
-// 128 x 128-byte boxes through a ring of shared-memory stages (tensor maps,
-// 128-byte swizzle, rows and columns past the matrix arrive as zeros); one
-// thread issues the matrix instructions; four consumer warps own 32 rows each,
-// one row a thread.
+// Below, P is the operand whose rows are the accumulator's rows (128 a CTA)
+// and Q the one whose rows are its columns (BN a tile). Three forms:
+//  - a pair of CTAs (CG = 2) shares 256 x 256 tiles: each loads half of either
+//    operand, so a tile's operands cross the L2 once for two SMs; a persistent
+//    grid walks the tiles;
+//  - one CTA a 128 x 128 tile, where there are too few tiles of the former;
+//  - SWAP: few rows of a. The weight b takes the P side, so that its rows fill
+//    the 128 accumulator rows, and a's rows are the narrow side.
+// The last two split k over the CTAs of a cluster where tiles are few: each
+// sums its share, and the shares are added through distributed shared memory
+// in rank order.
+//
+// Roles in a CTA, each a warp: the producer streams the operands' 128-byte
+// wide boxes through a ring of shared-memory stages (tensor maps, 128-byte
+// swizzle, rows and columns past the matrix arrive as zeros); a thread a
+// consumer group issues its matrix instructions; a warp brings the scales of
+// the next blocks to shared memory; four consumer warps a group own 32 rows
+// each, one row a thread and up to 128 columns.
+#include <algorithm>
 #include <atomic>
 
 #include "device_common.cuh"
@@ -22,208 +36,559 @@
 namespace ap {
 namespace {
 
-constexpr int kTile = 128;               // rows of a, rows of b and bytes of k in one stage
-constexpr int kMmaK = 32;                // k of one matrix instruction
-constexpr int kStages = 6;
-constexpr uint32_t kOperandBytes = kTile * kTile;
-constexpr uint32_t kStageBytes = 2 * kOperandBytes;
-constexpr int kConsumerWarps = 4;
-constexpr int kThreads = 32 * (kConsumerWarps + 2);
-constexpr uint32_t kTmemCols = 2 * kTile;  // two accumulators in turn
+constexpr int kTile = 128;  // rows a CTA, and bytes of k in one stage (one scale block)
+constexpr int kMmaK = 32;   // k of one matrix instruction
+constexpr int kMaxSplit = 8;
+constexpr int kScaleRun = 8;    // blocks of k whose scales are brought at once (one 32-byte sector of a row)
+constexpr int kScaleSlots = 2;  // such runs in shared memory
+constexpr int64_t kMaxTiles = int64_t(1) << 27;  // tile numbers plus a grid, times a cluster, stay in 32 bits
 
 struct MatmulParams {
-    const float* a_scales;
-    const float* b_scales;
+    const float* p_scales;
+    const float* q_scales;
     void* c;
-    int64_t m, n, ldc;
-    int32_t nkb;      // blocks of k
-    int32_t tiles_m;  // tiles along m
-    bool vec_c;       // rows of c start on 16-byte boundaries
-    uint32_t tx_extra;  // fault injection: bytes every stage waits for in vain
+    int64_t np, nq, ldc;  // rows of P and of Q
+    int p_shift;          // log2 of the rows of P that share a scale
+    int32_t nkb;          // blocks of k
+    int32_t tiles_p, tiles_q;
+    int split;            // CTAs of a cluster that share a tile's k
+    bool vec_c;           // rows of c start on 16-byte boundaries
+    uint32_t tx_extra;    // fault injection: bytes every stage waits for in vain
     uint64_t timeout_ns;
     uint32_t* status;
 };
 
-struct __align__(8) Shared {
-    uint64_t full[kStages], empty[kStages];
-    uint64_t acc_full[2], acc_empty[2];
+template <int BN, int CG, int STAGES, bool PER_COL>
+struct Form {
+    static constexpr int kGroups = BN > 128 ? 2 : 1;  // consumer groups, side by side along the columns
+    static constexpr int kCols = BN / kGroups;        // columns of a group, and of one matrix instruction
+    static constexpr int kConsumerWarps = 4 * kGroups;
+    static constexpr int kThreads = 32 * (kConsumerWarps + 4);
+    // Two groups: 384 threads of 168 registers at launch (64512), shared out
+    // anew: 128 sums and the loads under way need more than 168. With scales
+    // by column, 16 columns a load are what fits without spills.
+    static constexpr int kOtherRegs = PER_COL ? 56 : 72, kConsumerRegs = PER_COL ? 224 : 216;
+    static_assert(128 * kOtherRegs + 256 * kConsumerRegs <= 384 * 168, "registers of the launch");
+    static constexpr int kLoad = kCols < 32 || PER_COL ? 16 : 32;
+    static constexpr int kQBox = kCols / CG;  // rows of Q this CTA loads for a group
+    static constexpr uint32_t kPBytes = kTile * kTile, kQBytes = kQBox * kTile;
+    static constexpr uint32_t kStageBytes = kPBytes + kGroups * kQBytes;
+    // Accumulators in flight: a block's products wait in tensor memory from
+    // the matrix instructions' start until a consumer has read them, so the
+    // tensor core is kept busy when its 512 columns cover that time.
+    static constexpr int kBuffers = BN > 128 ? 2 : 4;
+    static constexpr uint32_t kTmemUsed = kBuffers * BN;
+    static constexpr uint32_t kTmemCols = kTmemUsed <= 64 ? 64 : (kTmemUsed <= 128 ? 128 : (kTmemUsed <= 256 ? 256 : 512));
+    // c leaves through shared memory: 4 KiB a consumer warp, 32 rows of 128 bytes
+    static constexpr uint32_t kStagingBytes = kCols >= 64 ? 4096 * kConsumerWarps : 0;
+    static constexpr size_t kRingBytes = size_t(STAGES) * kStageBytes;
+    static constexpr size_t kSmem = kRingBytes + kStagingBytes + 1024;
+    // a split tile's shares: rows of BN floats, padded so that the 32 rows a
+    // warp writes fall on different banks; or columns of 128 floats
+    static constexpr int kSharePitch = BN + 4;
+    static constexpr size_t kShareBytes = size_t(kTile) * kSharePitch * 4;
+};
+
+// Scales of a run of blocks, [slot][block][row or column]; the pitch puts the
+// eight blocks of four rows that a copy writes at once on different banks.
+template <typename F, int STAGES, bool PER_COL>
+struct __align__(16) Shared {
+    float row_scales[kScaleSlots][kScaleRun][kTile + 4];
+    float col_scales[kScaleSlots][kScaleRun][PER_COL ? F::kGroups * F::kCols + 4 : 4];  // or one a group
+    uint64_t full[STAGES], empty[STAGES];
+    uint64_t acc_full[F::kBuffers][F::kGroups], acc_empty[F::kBuffers][F::kGroups];
+    uint64_t scales_full[kScaleSlots], scales_empty[kScaleSlots];
     uint32_t tmem;
     int abort;
 };
 
-template <typename C, bool B_ROWS>
-__global__ void __launch_bounds__(kThreads, 1)
-    matmul_fp8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                      const __grid_constant__ MatmulParams P) {
+// Tile t of the walk: bands of 8 tiles along P, Q outermost within a band, so
+// the CTAs of one moment share operand rows in the L2.
+__device__ __forceinline__ void tile_at(const MatmulParams& P, int32_t t, int32_t* tp, int32_t* tq) {
+    constexpr int kBand = 8;
+    const int32_t per_band = kBand * P.tiles_q;
+    const int32_t first = t / per_band * kBand;
+    const int32_t high = P.tiles_p - first < kBand ? P.tiles_p - first : kBand;
+    const int32_t r = t % per_band;
+    *tp = first + r % high;
+    *tq = r / high;
+}
+
+// Four values as the C type at p (aligned for a vector store).
+template <typename C>
+__device__ __forceinline__ void store4(C* p, float4 v) {
+    if constexpr (sizeof(C) == 4)
+        *reinterpret_cast<float4*>(p) = v;
+    else
+        *reinterpret_cast<uint2*>(p) = make_uint2(pack2<C>(v.x, v.y), pack2<C>(v.z, v.w));
+}
+
+__device__ __forceinline__ uint4 as_words(float a, float b, float c, float d) {
+    return make_uint4(__float_as_uint(a), __float_as_uint(b), __float_as_uint(c), __float_as_uint(d));
+}
+
+__device__ __forceinline__ void st_shared(uint32_t addr, float v) {
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ void st_shared4(uint32_t addr, uint4 v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+template <typename C, int BN, int CG, int STAGES, bool PER_COL, bool SWAP>
+__global__ void __launch_bounds__(Form<BN, CG, STAGES, PER_COL>::kThreads, 1)
+    matmul_fp8_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
+                      const __grid_constant__ CUtensorMap map_c, const __grid_constant__ MatmulParams P) {
+    using F = Form<BN, CG, STAGES, PER_COL>;
+    constexpr int kCols = F::kCols;
     extern __shared__ unsigned char smem_raw[];
-    __shared__ Shared sh;
-    __shared__ float col_scales[2][kTile];
+    __shared__ Shared<F, STAGES, PER_COL> sh;
     const uint32_t ring = (ptx::smem_addr(smem_raw) + 1023u) & ~1023u;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int32_t m0 = static_cast<int32_t>(blockIdx.x % P.tiles_m) * kTile;
-    const int32_t n0 = static_cast<int32_t>(blockIdx.x / P.tiles_m) * kTile;
     volatile int* abort_flag = &sh.abort;
+    const uint32_t rank = CG == 2 || P.split > 1 ? ptx::cluster_ctarank() : 0;
+    const int part = CG == 2 ? 0 : static_cast<int>(rank);  // share of k
+    const int32_t kb0 = static_cast<int32_t>(static_cast<int64_t>(P.nkb) * part / P.split);
+    const int32_t kb1 = static_cast<int32_t>(static_cast<int64_t>(P.nkb) * (part + 1) / P.split);
+    const int32_t tiles = P.tiles_p * P.tiles_q;  // at most kMaxTiles
+    const int32_t per_tile = CG == 2 ? 2 : P.split;  // CTAs of a cluster
+    const int32_t first_tile = static_cast<int32_t>(blockIdx.x) / per_tile;
+    const int32_t tile_step = static_cast<int32_t>(gridDim.x) / per_tile;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) {
+        for (int s = 0; s < STAGES; ++s) {
             ptx::mbar_init(ptx::smem_addr(&sh.full[s]), 1);
-            ptx::mbar_init(ptx::smem_addr(&sh.empty[s]), 1);
+            ptx::mbar_init(ptx::smem_addr(&sh.empty[s]), F::kGroups);
         }
-        for (int s = 0; s < 2; ++s) {
-            ptx::mbar_init(ptx::smem_addr(&sh.acc_full[s]), 1);
-            ptx::mbar_init(ptx::smem_addr(&sh.acc_empty[s]), kConsumerWarps);
+        for (int g = 0; g < F::kGroups; ++g) {
+            for (int s = 0; s < F::kBuffers; ++s) {
+                ptx::mbar_init(ptx::smem_addr(&sh.acc_full[s][g]), 1);
+                ptx::mbar_init(ptx::smem_addr(&sh.acc_empty[s][g]), CG * 4);
+            }
+        }
+        for (int s = 0; s < kScaleSlots; ++s) {
+            ptx::mbar_init(ptx::smem_addr(&sh.scales_full[s]), 32);
+            ptx::mbar_init(ptx::smem_addr(&sh.scales_empty[s]), F::kConsumerWarps);
         }
         sh.abort = 0;
         ptx::fence_mbar_init();
     }
-    if (warp == kConsumerWarps) {
-        ptx::tmem_alloc(ptx::smem_addr(&sh.tmem), kTmemCols);
-        ptx::tmem_relinquish();
-    }
+    if (warp == F::kConsumerWarps + 1) ptx::tmem_alloc<CG>(ptx::smem_addr(&sh.tmem), F::kTmemCols);
     ptx::tcgen05_fence_before();
     __syncthreads();
+    if (CG == 2) ptx::cluster_sync();  // the other CTA's barriers are ready too
     ptx::tcgen05_fence_after();
     const uint32_t tmem = sh.tmem;
 
-    // A wait that gives up ends its role; the CTA's abort flag ends the others.
+    // A wait that gives up ends its role; the CTA's abort flag ends the
+    // others. The first probes go without wait_phase's clock reads.
     auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
+        for (int i = 0; i < 64; ++i)
+            if (ptx::mbar_try_wait(ptx::smem_addr(bar), parity)) return true;
         const int w = wait_phase<false>(ptx::smem_addr(bar), parity, P.timeout_ns, abort_flag);
         if (w == WAIT_TIMEOUT) raise_timeout(P.status, site, abort_flag);
         return w == WAIT_OK;
     };
 
-    if (warp == kConsumerWarps + 1) {
-        if (lane == 0) {  // producer
-            int issued = 0;
-            for (; issued < P.nkb; ++issued) {
-                const int s = issued % kStages;
-                const uint32_t round = static_cast<uint32_t>(issued / kStages);
-                if (round > 0 && !wait(&sh.empty[s], (round - 1) & 1, SITE_MM_PRODUCER_EMPTY)) break;
-                const uint32_t bar = ptx::smem_addr(&sh.full[s]);
-                ptx::mbar_arrive_expect_tx(bar, kStageBytes + P.tx_extra);
-                ptx::tensor_g2s_2d(ring + s * kStageBytes, &map_a, issued * kTile, m0, bar);
-                ptx::tensor_g2s_2d(ring + s * kStageBytes + kOperandBytes, &map_b, issued * kTile, n0, bar);
-            }
-            // nothing may still be landing in this CTA's shared memory or
-            // arriving on its barriers when it leaves
-            for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i) {
-                const uint32_t parity = static_cast<uint32_t>(i / kStages) & 1;
-                if (!drain_wait<false>(ptx::smem_addr(&sh.full[i % kStages]), parity, P.timeout_ns, P.status,
-                                       SITE_MM_DRAIN, abort_flag) ||
-                    !drain_wait<false>(ptx::smem_addr(&sh.empty[i % kStages]), parity, P.timeout_ns, P.status,
-                                       SITE_MM_DRAIN, abort_flag))
-                    break;
-            }
-        }
-    } else if (warp == kConsumerWarps) {
-        if (lane == 0) {  // matrix instructions
-            constexpr uint32_t idesc = ptx::e4m3_instr_desc(kTile, kTile);
-            for (int kb = 0; kb < P.nkb; ++kb) {
-                const int s = kb % kStages, buf = kb & 1;
-                const uint32_t turn = static_cast<uint32_t>(kb >> 1);
-                if (turn > 0 && !wait(&sh.acc_empty[buf], (turn - 1) & 1, SITE_MM_MMA_ACC)) break;
-                if (!wait(&sh.full[s], static_cast<uint32_t>(kb / kStages) & 1, SITE_MM_MMA_FULL)) break;
-                ptx::tcgen05_fence_after();
-                const uint64_t da = ptx::operand_desc(ring + s * kStageBytes);
-                const uint64_t db = ptx::operand_desc(ring + s * kStageBytes + kOperandBytes);
+    // For a whole warp: one lane asks, since 32 lanes' probes of a barrier are
+    // served one after another and hold up every other barrier of the SM.
+    auto warp_wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
+        bool ok = true;
+        if (lane == 0) ok = wait(bar, parity, site);
+        return __shfl_sync(0xffffffffu, static_cast<int>(ok), 0) != 0;
+    };
+
+    if (warp >= F::kConsumerWarps) {
+        if (F::kGroups == 2) ptx::regs_less<F::kOtherRegs>();
+        if (warp == F::kConsumerWarps) {
+            if (ptx::elect_one()) {  // producer
+                uint32_t it = 0;
+                bool ready = true, ok = true;
+                for (int32_t t = first_tile; t < tiles && ok; t += tile_step) {
+                    int32_t tp, tq;
+                    tile_at(P, t, &tp, &tq);
+                    const int32_t p0 = (tp * CG + (CG == 2 ? static_cast<int32_t>(rank) : 0)) * kTile;
+                    const int32_t q0 = tq * BN + (CG == 2 ? static_cast<int32_t>(rank) * F::kQBox : 0);
+                    for (int32_t kb = kb0; kb < kb1; ++kb, ++it) {
+                        const uint32_t s = it % STAGES;
+                        if (!ready && !wait(&sh.empty[s], (it / STAGES - 1) & 1, SITE_MM_PRODUCER_EMPTY)) {
+                            ok = false;
+                            break;
+                        }
+                        uint32_t bar = ptx::smem_addr(&sh.full[s]);
+                        // a pair's stage is complete when both CTAs' boxes
+                        // have landed; the even CTA's barrier counts them all
+                        if (rank == 0 || CG == 1) ptx::mbar_arrive_expect_tx(bar, CG * F::kStageBytes + P.tx_extra);
+                        if (CG == 2) bar = ptx::mapa(bar, 0);
+                        const uint32_t dst = ring + s * F::kStageBytes;
+                        ptx::operand_g2s<CG>(dst, &map_p, kb * kTile, p0, bar);
 #pragma unroll
-                for (int k = 0; k < kTile / kMmaK; ++k)
-                    ptx::mma_e4m3(tmem + buf * kTile, da + k * (kMmaK >> 4), db + k * (kMmaK >> 4), idesc, k > 0);
-                ptx::mma_commit(ptx::smem_addr(&sh.empty[s]));
-                ptx::mma_commit(ptx::smem_addr(&sh.acc_full[buf]));
-            }
-        }
-    } else {  // consumers: thread = row m0 + 32 * warp + lane, all columns
-        const int64_t row = m0 + 32 * warp + lane;
-        const float* sa = P.a_scales + (row < P.m ? row : P.m - 1) * P.nkb;
-        const int64_t my_col = n0 + 32 * warp + lane;  // B_ROWS: the column whose scales this thread fetches
-        const float* sb = B_ROWS ? P.b_scales + (my_col < P.n ? my_col : P.n - 1) * P.nkb
-                                 : P.b_scales + static_cast<int64_t>(n0 / kTile) * P.nkb;
-        float acc[kTile];
-#pragma unroll
-        for (int j = 0; j < kTile; ++j) acc[j] = 0.0f;
-        for (int kb = 0; kb < P.nkb; ++kb) {
-            const int buf = kb & 1;
-            float scale = sa[kb];
-            if (B_ROWS) {
-                col_scales[buf][32 * warp + lane] = sb[kb];
-                ptx::named_barrier_sync(1, 32 * kConsumerWarps);
-            } else {
-                scale *= sb[kb];
-            }
-            // a lane that gave up must not leave its warp's collective loads
-            const bool ok = wait(&sh.acc_full[buf], static_cast<uint32_t>(kb >> 1) & 1, SITE_MM_CONSUMER_ACC);
-            if (!B_ROWS && !__all_sync(0xffffffffu, ok)) break;
-            if (__all_sync(0xffffffffu, ok)) {
-                ptx::tcgen05_fence_after();
-                const uint32_t at = tmem + buf * kTile + (static_cast<uint32_t>(32 * warp) << 16);
-                float v[2][16];
-                ptx::tmem_ld16(at, v[0]);
-#pragma unroll
-                for (int g = 0; g < kTile / 16; ++g) {
-                    ptx::tmem_wait_ld(v[g & 1]);
-                    if (g + 1 < kTile / 16) ptx::tmem_ld16(at + 16 * (g + 1), v[(g + 1) & 1]);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int j = 16 * g + i;
-                        acc[j] = fmaf(v[g & 1][i], B_ROWS ? scale * col_scales[buf][j] : scale, acc[j]);
+                        for (int g = 0; g < F::kGroups; ++g)
+                            ptx::operand_g2s<CG>(dst + F::kPBytes + g * F::kQBytes, &map_q, kb * kTile, q0 + g * kCols, bar);
+                        const uint32_t next = it + 1;
+                        ready = next < STAGES || ptx::mbar_test(ptx::smem_addr(&sh.empty[next % STAGES]), (next / STAGES - 1) & 1);
                     }
                 }
-                ptx::tcgen05_fence_before();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&sh.acc_empty[buf]));
+                // Nothing may still be landing in this CTA's shared memory or
+                // arriving on its barriers when it leaves: a stage is released
+                // after its boxes have landed and been read.
+                for (uint32_t i = it > STAGES ? it - STAGES : 0; i < it; ++i)
+                    if (!drain_wait<false>(ptx::smem_addr(&sh.empty[i % STAGES]), (i / STAGES) & 1, P.timeout_ns, P.status,
+                                           SITE_MM_DRAIN, abort_flag))
+                        break;
             }
-        }
-        if (row < P.m && !*abort_flag) {
-            C* out = static_cast<C*>(P.c) + row * P.ldc + n0;
+        } else if (warp - F::kConsumerWarps - 1 < F::kGroups) {
+            // Matrix instructions, a warp a group: a block's accumulator and
+            // stage barriers cost one thread more than the instructions take.
+            const int g = warp - F::kConsumerWarps - 1;
+            if ((CG == 1 || rank == 0) && ptx::elect_one()) {
+                constexpr uint32_t idesc = ptx::e4m3_instr_desc(CG * kTile, kCols);
+                uint32_t it = 0;
+                bool ok = true;
+                for (int32_t t = first_tile; t < tiles && ok; t += tile_step) {
+                    for (int32_t kb = kb0; kb < kb1; ++kb, ++it) {
+                        const uint32_t s = it % STAGES, buf = it % F::kBuffers, turn = it / F::kBuffers;
+                        if ((turn > 0 && !wait(&sh.acc_empty[buf][g], (turn - 1) & 1, SITE_MM_MMA_ACC)) ||
+                            !wait(&sh.full[s], (it / STAGES) & 1, SITE_MM_MMA_FULL)) {
+                            ok = false;
+                            break;
+                        }
+                        ptx::tcgen05_fence_after();
+                        const uint64_t dp = ptx::operand_desc(ring + s * F::kStageBytes);
+                        const uint64_t dq = ptx::operand_desc(ring + s * F::kStageBytes + F::kPBytes + g * F::kQBytes);
 #pragma unroll
-            for (int j = 0; j < kTile; j += 8) {
-                const int64_t left = P.n - n0 - j;
-                if (left > 0) store8(out + j, P.vec_c, left, *reinterpret_cast<const float(*)[8]>(&acc[j]));
+                        for (int k = 0; k < kTile / kMmaK; ++k)
+                            ptx::mma_e4m3<CG>(tmem + (buf * F::kGroups + g) * kCols, dp + k * (kMmaK >> 4),
+                                              dq + k * (kMmaK >> 4), idesc, k > 0);
+                        ptx::mma_commit<CG>(ptx::smem_addr(&sh.acc_full[buf][g]));
+                        ptx::mma_commit<CG>(ptx::smem_addr(&sh.empty[s]));
+                    }
+                }
+            }
+        } else if (warp == F::kConsumerWarps + 3) {
+            // Scales, by 4-byte asynchronous copies: lane l brings block l % 8
+            // of every fourth row, so that a copy touches four rows (a sector
+            // or two each) whatever their alignment, and all of a run are in
+            // flight at once.
+            const int e = lane & 7, r4 = lane >> 3;
+            uint32_t run = 0;
+            bool ok = true;
+            for (int32_t t = first_tile; t < tiles && ok; t += tile_step) {
+                int32_t tp, tq;
+                tile_at(P, t, &tp, &tq);
+                const int64_t p0 = (static_cast<int64_t>(tp) * CG + (CG == 2 ? rank : 0)) * kTile;
+                const int64_t q0 = static_cast<int64_t>(tq) * BN;
+                for (int32_t kb = kb0; kb < kb1; kb += kScaleRun, ++run) {
+                    const uint32_t slot = run % kScaleSlots;
+                    ok = run < kScaleSlots || warp_wait(&sh.scales_empty[slot], (run / kScaleSlots - 1) & 1, SITE_MM_SCALES_EMPTY);
+                    if (!ok) break;
+                    const int32_t at = kb + e < kb1 ? kb + e : kb;  // past the end: any valid block
+#pragma unroll 4
+                    for (int i = 0; i < kTile; i += 4) {
+                        const int64_t row = p0 + i + r4;
+                        ptx::cp_async_ca4(ptx::smem_addr(&sh.row_scales[slot][e][i + r4]),
+                                          P.p_scales + ((row < P.np ? row : P.np - 1) >> P.p_shift) * P.nkb + at);
+                    }
+                    if (PER_COL) {
+#pragma unroll 4
+                        for (int i = 0; i < BN; i += 4) {
+                            const int64_t col = q0 + i + r4;
+                            ptx::cp_async_ca4(ptx::smem_addr(&sh.col_scales[slot][e][PER_COL ? i + r4 : 0]),
+                                              P.q_scales + (col < P.nq ? col : P.nq - 1) * P.nkb + at);
+                        }
+                    } else if (r4 < F::kGroups) {
+                        const int64_t col = q0 + r4 * kCols;
+                        ptx::cp_async_ca4(ptx::smem_addr(&sh.col_scales[slot][e][r4]),
+                                          P.q_scales + (col < P.nq ? col : P.nq - 1) / kTile * P.nkb + at);
+                    }
+                    ptx::cp_async_mbar_arrive_noinc(ptx::smem_addr(&sh.scales_full[slot]));
+                }
+            }
+            ptx::cp_async_wait_all();
+        }
+    } else {  // consumers
+        if (F::kGroups == 2) ptx::regs_more<F::kConsumerRegs>();
+        constexpr int kLoad = F::kLoad;  // columns of one load from tensor memory
+        constexpr int kLoads = kCols / kLoad;
+        const int group = warp / 4, quad = warp % 4;
+        const int my_row = 32 * quad + lane;  // accumulator row of this thread, in the CTA's 128
+        const uint32_t staging = ring + static_cast<uint32_t>(F::kRingBytes) + 4096u * warp;
+        uint32_t it = 0, run = 0;
+        bool ok = true;
+        for (int32_t t = first_tile; t < tiles; t += tile_step) {
+            int32_t tp, tq;
+            tile_at(P, t, &tp, &tq);
+            float acc[kCols];
+#pragma unroll
+            for (int j = 0; j < kCols; ++j) acc[j] = 0.0f;
+            // A warp takes the blocks one after another, so what it waits for
+            // is taken off that path: the next block's barrier is asked before
+            // this block's sums, the next load from tensor memory (the next
+            // block's first one included) is under way while the sums of the
+            // current one are taken, and nothing on the path branches by lane.
+            float v[2][kLoad];
+            const uint32_t lanes = tmem + group * kCols + (static_cast<uint32_t>(32 * quad) << 16);
+            ok = ok && warp_wait(&sh.acc_full[it % F::kBuffers][group], (it / F::kBuffers) & 1, SITE_MM_CONSUMER_ACC);
+            ok = ok && warp_wait(&sh.scales_full[run % kScaleSlots], (run / kScaleSlots) & 1, SITE_MM_SCALES_FULL);
+            if (ok) {
+                ptx::tcgen05_fence_after();
+                ptx::tmem_ld(lanes + (it % F::kBuffers) * BN, v[0]);
+            }
+            for (int32_t kb = kb0; kb < kb1 && ok; ++kb, ++it) {
+                const uint32_t buf = it % F::kBuffers, slot = run % kScaleSlots;
+                const uint32_t next = it + 1, next_buf = next % F::kBuffers;
+                const int e = (kb - kb0) % kScaleRun;
+                const bool last = kb + 1 == kb1;
+                bool ready = ptx::mbar_test(ptx::smem_addr(&sh.acc_full[next_buf][group]), (next / F::kBuffers) & 1);
+                float scale = sh.row_scales[slot][e][my_row];
+                if (!PER_COL) scale *= sh.col_scales[slot][e][group];
+#pragma unroll
+                for (int g = 0; g < kLoads; ++g) {
+                    ptx::tmem_wait_ld(v[g % 2]);
+                    if (g + 1 < kLoads) {
+                        ptx::tmem_ld(lanes + buf * BN + kLoad * (g + 1), v[(g + 1) % 2]);
+                    } else {
+                        // all of the accumulator is in registers: it is free
+                        // before the last sums are taken
+                        ptx::tcgen05_fence_before();
+                        __syncwarp();
+                        const uint32_t bar = ptx::smem_addr(&sh.acc_empty[buf][group]);
+                        ptx::mbar_arrive_if<CG == 2>(lane == 0, CG == 2 ? ptx::mapa(bar, 0) : bar);
+                        if (!last) {
+                            if (!ready) ready = wait(&sh.acc_full[next_buf][group], (next / F::kBuffers) & 1, SITE_MM_CONSUMER_ACC);
+                            ok = __all_sync(0xffffffffu, ready);
+                            ptx::tcgen05_fence_after();
+                            if (ok && kLoads % 2 == 0) ptx::tmem_ld(lanes + next_buf * BN, v[0]);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < kLoad; i += 4) {
+                        const int j = kLoad * g + i;
+                        float4 cs = make_float4(scale, scale, scale, scale);
+                        if (PER_COL) {
+                            cs = *reinterpret_cast<const float4*>(&sh.col_scales[slot][e][PER_COL ? group * kCols + j : 0]);
+                            cs.x *= scale, cs.y *= scale, cs.z *= scale, cs.w *= scale;
+                        }
+                        acc[j] = fmaf(v[g % 2][i], cs.x, acc[j]);
+                        acc[j + 1] = fmaf(v[g % 2][i + 1], cs.y, acc[j + 1]);
+                        acc[j + 2] = fmaf(v[g % 2][i + 2], cs.z, acc[j + 2]);
+                        acc[j + 3] = fmaf(v[g % 2][i + 3], cs.w, acc[j + 3]);
+                    }
+                }
+                // one load a block: its registers are free only now
+                if (kLoads % 2 != 0 && ok && !last) ptx::tmem_ld(lanes + next_buf * BN, v[0]);
+                if (e == kScaleRun - 1 || last) {  // this run's scales have been read
+                    __syncwarp();
+                    ptx::mbar_arrive_if<false>(lane == 0, ptx::smem_addr(&sh.scales_empty[slot]));
+                    ++run;
+                    if (!last && ok) {
+                        uint64_t* bar = &sh.scales_full[run % kScaleSlots];
+                        ok = __all_sync(0xffffffffu, wait(bar, (run / kScaleSlots) & 1, SITE_MM_SCALES_FULL));
+                    }
+                }
+            }
+            const int64_t row = (static_cast<int64_t>(tp) * CG + (CG == 2 ? rank : 0)) * kTile + my_row;
+            const int64_t q0 = static_cast<int64_t>(tq) * BN + group * kCols;  // this group's first column
+            if (CG == 1 && P.split > 1) {
+                // this CTA's share, into the ring (every stage has been read:
+                // the last accumulator is complete)
+#pragma unroll
+                for (int j = 0; j < kCols; j += 4) {
+                    const int col = group * kCols + j;
+                    if (SWAP) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) st_shared(ring + 4 * ((col + i) * kTile + my_row), acc[j + i]);
+                    } else {
+                        st_shared4(ring + 4 * (my_row * F::kSharePitch + col), as_words(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]));
+                    }
+                }
+            } else if (!SWAP && F::kStagingBytes > 0 && P.vec_c) {
+                // 32 rows x 128 bytes at a time through the warp's staging:
+                // 16-byte units at the places the tensor map's swizzle gives
+                // them, so a warp's writes meet no bank twice
+                constexpr int kPiece = 128 / sizeof(C), kUnit = 16 / sizeof(C);
+                if (ok) {
+#pragma unroll
+                    for (int piece = 0; piece < (F::kStagingBytes > 0 ? kCols / kPiece : 0); ++piece) {
+                        if (lane == 0) ptx::bulk_wait_read<0>();  // the previous piece has left
+                        __syncwarp();
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) {
+                            const int j = piece * kPiece + u * kUnit;
+                            uint4 w;
+                            if constexpr (sizeof(C) == 4)
+                                w = as_words(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+                            else
+                                w = make_uint4(pack2<C>(acc[j], acc[j + 1]), pack2<C>(acc[j + 2], acc[j + 3]),
+                                               pack2<C>(acc[j + 4], acc[j + 5]), pack2<C>(acc[j + 6], acc[j + 7]));
+                            st_shared4(staging + 128 * lane + 16 * (u ^ (lane & 7)), w);
+                        }
+                        ptx::fence_proxy_async_smem();
+                        __syncwarp();
+                        const int64_t row0 = row - lane, col0 = q0 + piece * kPiece;
+                        if (lane == 0 && row0 < P.np && col0 < P.nq) {
+                            ptx::tensor_s2g_2d(&map_c, static_cast<int32_t>(col0), static_cast<int32_t>(row0), staging);
+                            ptx::bulk_commit();
+                        }
+                    }
+                }
+            } else if (ok && row < P.np) {
+#pragma unroll
+                for (int j = 0; j < kCols; j += 8) {
+                    float v[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] = acc[j + i];
+                    const int64_t left = P.nq - q0 - j;
+                    if (SWAP) {  // the threads of a warp write 32 neighbours of one row of c
+                        C* out = static_cast<C*>(P.c) + (q0 + j) * P.ldc + row;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (i < left) out[i * P.ldc] = from_f32<C>(v[i]);
+                    } else if (left > 0) {
+                        store8(static_cast<C*>(P.c) + row * P.ldc + q0 + j, false, left, v);
+                    }
+                }
             }
         }
+        if (!SWAP && F::kStagingBytes > 0 && lane == 0) ptx::bulk_wait_all();
     }
     __syncwarp();  // the one-thread roles' idle lanes wait here
     ptx::tcgen05_fence_before();
     __syncthreads();
     ptx::tcgen05_fence_after();
-    if (warp == kConsumerWarps) ptx::tmem_dealloc(tmem, kTmemCols);
+    if (CG == 2) ptx::cluster_sync();  // neither CTA's memory goes while the other may still use or signal it
+    if (warp == F::kConsumerWarps + 1) ptx::tmem_dealloc<CG>(tmem, F::kTmemCols);
+    if (CG == 1 && P.split > 1) {
+        ptx::cluster_sync();  // every share is written
+        if (warp < F::kConsumerWarps && !*abort_flag) {
+            int32_t tp, tq;
+            tile_at(P, first_tile, &tp, &tq);
+            const int64_t p0 = static_cast<int64_t>(tp) * kTile, q0 = static_cast<int64_t>(tq) * BN;
+            if (SWAP) {  // columns of this rank: a thread a row
+                const int c0 = BN * part / P.split, c1 = BN * (part + 1) / P.split;
+                const int my_row = threadIdx.x & 127;
+                for (int c = c0 + (threadIdx.x >> 7); c < c1; c += F::kGroups) {
+                    float v = 0.0f;
+                    for (int r = 0; r < P.split; ++r) v += ptx::cluster_ld(ptx::mapa(ring + 4 * (c * kTile + my_row), r));
+                    if (p0 + my_row < P.np && q0 + c < P.nq)
+                        static_cast<C*>(P.c)[(q0 + c) * P.ldc + p0 + my_row] = from_f32<C>(v);
+                }
+            } else {  // rows of this rank: a warp a row, four columns a lane
+                const int r0 = kTile * part / P.split, r1 = kTile * (part + 1) / P.split;
+                for (int i = r0 + warp; i < r1 && p0 + i < P.np; i += F::kConsumerWarps) {
+                    for (int c = 4 * lane; c < BN; c += 128) {
+                        float4 v = make_float4(0, 0, 0, 0);
+                        for (int r = 0; r < P.split; ++r) {
+                            const float4 w = ptx::cluster_ld4(ptx::mapa(ring + 4 * (i * F::kSharePitch + c), r));
+                            v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+                        }
+                        C* out = static_cast<C*>(P.c) + (p0 + i) * P.ldc + q0 + c;
+                        const int64_t left = P.nq - q0 - c;
+                        if (P.vec_c && left >= 4) {
+                            store4(out, v);
+                        } else {
+                            const float u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (e < left) out[e] = from_f32<C>(u[e]);
+                        }
+                    }
+                }
+            }
+        }
+        ptx::cluster_sync();  // every share has been read
+    }
 }
 
-// A rows x k byte matrix as boxes of 128 bytes by box_rows rows.
-bool operand_map(CUtensorMap* map, const uint8_t* p, int64_t rows, int64_t k, int64_t ld, uint32_t box_rows) {
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld)};
-    const cuuint32_t box[2] = {static_cast<cuuint32_t>(kTile), box_rows};
+// A matrix of rows x cols elements as boxes of 128 bytes by box_rows rows.
+bool box_map(CUtensorMap* map, CUtensorMapDataType type, const void* p, int64_t size, int64_t rows, int64_t cols, int64_t ld,
+             uint32_t box_rows) {
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld * size)};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / size), box_rows};
     const cuuint32_t estr[2] = {1, 1};
     auto encode = tensor_map_encoder();
     return encode != nullptr &&
-           encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(p), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+           encode(map, type, 2, const_cast<void*>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename C, bool B_ROWS>
-ap_status launch_mm(const DeviceInfo& di, const MatmulParams& P, const CUtensorMap& ma, const CUtensorMap& mb,
-                    int64_t grid, cudaStream_t stream) {
-    constexpr size_t smem = kStages * kStageBytes + 1024;
+template <typename C, int BN, int CG, int STAGES, bool PER_COL, bool SWAP>
+ap_status launch_form(const DeviceInfo& di, MatmulParams P, const MatmulArgs& a, int split, cudaStream_t stream) {
+    using F = Form<BN, CG, STAGES, PER_COL>;
+    static_assert(F::kSmem + sizeof(Shared<F, STAGES, PER_COL>) <= kSmemOptinGB300, "shared memory of a CTA");
+    static_assert(CG == 2 || F::kShareBytes <= F::kRingBytes, "a share fits in the ring");
+    P.np = SWAP ? a.n : a.m;
+    P.nq = SWAP ? a.m : a.n;
+    P.p_scales = SWAP ? a.b_scales : a.a_scales;
+    P.q_scales = SWAP ? a.a_scales : a.b_scales;
+    P.p_shift = SWAP && a.b_block_rows != 1 ? 7 : 0;
+    const int64_t tiles_p = (P.np + CG * kTile - 1) / (CG * kTile), tiles_q = (P.nq + BN - 1) / BN;
+    P.tiles_p = static_cast<int32_t>(tiles_p);
+    P.tiles_q = static_cast<int32_t>(tiles_q);
+    P.split = split;
+    CUtensorMap mp, mq, mc{};
+    constexpr auto codes = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    if (!box_map(&mp, codes, SWAP ? a.b : a.a, 1, P.np, a.k, SWAP ? a.ldb : a.lda, kTile) ||
+        !box_map(&mq, codes, SWAP ? a.a : a.b, 1, P.nq, a.k, SWAP ? a.lda : a.ldb, F::kQBox))
+        return AP_ERR_CUDA;
+    if (!SWAP && split == 1 && P.vec_c &&
+        !box_map(&mc, sizeof(C) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, a.c, sizeof(C), a.m,
+                 a.n, a.ldc, 32))
+        return AP_ERR_CUDA;
+    auto kernel = matmul_fp8_kernel<C, BN, CG, STAGES, PER_COL, SWAP>;
     static std::atomic<int> configured[64];  // attribute set on this device (setting twice is harmless)
     if (di.device < 0 || di.device >= 64) return AP_ERR_CUDA;
     if (!configured[di.device].load()) {
-        if (cudaFuncSetAttribute(matmul_fp8_kernel<C, B_ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(smem)) != cudaSuccess)
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(F::kSmem)) !=
+            cudaSuccess)
             return AP_ERR_CUDA;
         configured[di.device] = 1;
     }
-    record_launch(PATH_MATMUL, grid, kTile, static_cast<int64_t>(smem), kStages, B_ROWS ? 1 : 0);
-    matmul_fp8_kernel<C, B_ROWS><<<static_cast<unsigned>(grid), kThreads, smem, stream>>>(ma, mb, P);
-    return cudaGetLastError() == cudaSuccess ? AP_OK : AP_ERR_CUDA;
+    const int64_t tiles = tiles_p * tiles_q;
+    if (tiles > kMaxTiles) return AP_ERR_SHAPE;
+    const int cluster = CG == 2 ? 2 : split;
+    int64_t grid = tiles * cluster;
+    if (split == 1) grid = std::min<int64_t>(grid, di.sms / cluster * cluster);
+    record_launch(PATH_MATMUL, grid, BN, static_cast<int64_t>(F::kSmem), STAGES, (SWAP ? 1 : 0) | (CG == 2 ? 2 : 0) | split << 4);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(F::kThreads);
+    cfg.dynamicSmemBytes = F::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, mp, mq, mc, P) == cudaSuccess ? AP_OK : AP_ERR_CUDA;
+}
+
+// CTAs of a cluster that share a tile's k: as many as keep the SMs busy, each
+// with at least two blocks of k.
+int split_for(const DeviceInfo& di, int64_t tiles, int64_t nkb) {
+    int split = 1;
+    while (split < kMaxSplit && tiles * split * 2 <= di.sms && nkb >= 4 * split) split *= 2;
+    return split;
 }
 
 template <typename C>
-ap_status launch_mm_c(const DeviceInfo& di, const MatmulParams& P, const CUtensorMap& ma, const CUtensorMap& mb,
-                      int64_t grid, bool b_rows, cudaStream_t stream) {
-    return b_rows ? launch_mm<C, true>(di, P, ma, mb, grid, stream) : launch_mm<C, false>(di, P, ma, mb, grid, stream);
+ap_status launch_mm(const DeviceInfo& di, const MatmulParams& P, const MatmulArgs& a, cudaStream_t stream) {
+    const auto tiles_of = [&](int64_t pr, int64_t p, int64_t qr, int64_t q) { return (pr + p - 1) / p * ((qr + q - 1) / q); };
+    const bool rows = a.b_block_rows == 1;
+    if (a.m <= 64) {
+        const int64_t bn = a.m <= 16 ? 16 : (a.m <= 32 ? 32 : 64);
+        const int split = split_for(di, tiles_of(a.n, kTile, a.m, bn), P.nkb);
+        if (a.m <= 16) return launch_form<C, 16, 1, 10, true, true>(di, P, a, split, stream);
+        if (a.m <= 32) return launch_form<C, 32, 1, 9, true, true>(di, P, a, split, stream);
+        return launch_form<C, 64, 1, 7, true, true>(di, P, a, split, stream);
+    }
+    if (tiles_of(a.m, 2 * kTile, a.n, 256) >= di.sms / 4)
+        return rows ? launch_form<C, 256, 2, 5, true, false>(di, P, a, 1, stream)
+                    : launch_form<C, 256, 2, 5, false, false>(di, P, a, 1, stream);
+    const int split = split_for(di, tiles_of(a.m, kTile, a.n, kTile), P.nkb);
+    return rows ? launch_form<C, 128, 1, 5, true, false>(di, P, a, split, stream)
+                : launch_form<C, 128, 1, 5, false, false>(di, P, a, split, stream);
 }
 
 }  // namespace
@@ -236,29 +601,18 @@ ap_status launch_matmul_fp8(const DeviceInfo& di, const Options& o, const Matmul
                    ? AP_OK
                    : AP_ERR_CUDA;
     }
-    MatmulParams P;
-    P.a_scales = a.a_scales;
-    P.b_scales = a.b_scales;
+    MatmulParams P{};
     P.c = a.c;
-    P.m = a.m;
-    P.n = a.n;
     P.ldc = a.ldc;
     P.nkb = static_cast<int32_t>((a.k + kTile - 1) / kTile);
-    P.tiles_m = static_cast<int32_t>((a.m + kTile - 1) / kTile);
     P.vec_c = rows_aligned(a.c, a.ldc, size, 16);
     P.tx_extra = static_cast<uint32_t>(o.tx_extra);
     P.timeout_ns = static_cast<uint64_t>(o.timeout_ns);
     P.status = di.status;
-    const int64_t grid = P.tiles_m * ((a.n + kTile - 1) / kTile);
-    if (grid >= (int64_t(1) << 31)) return AP_ERR_SHAPE;
-    CUtensorMap ma, mb;
-    if (!operand_map(&ma, a.a, a.m, a.k, a.lda, kTile) || !operand_map(&mb, a.b, a.n, a.k, a.ldb, kTile))
-        return AP_ERR_CUDA;
-    const bool b_rows = a.b_block_rows == 1;
     switch (a.c_type) {
-        case AP_BF16: return launch_mm_c<__nv_bfloat16>(di, P, ma, mb, grid, b_rows, stream);
-        case AP_F16: return launch_mm_c<__half>(di, P, ma, mb, grid, b_rows, stream);
-        default: return launch_mm_c<float>(di, P, ma, mb, grid, b_rows, stream);
+        case AP_BF16: return launch_mm<__nv_bfloat16>(di, P, a, stream);
+        case AP_F16: return launch_mm<__half>(di, P, a, stream);
+        default: return launch_mm<float>(di, P, a, stream);
     }
 }
 
