@@ -140,6 +140,15 @@ ap_status launch_fma_probe_horner(const DeviceInfo& di, float* out, int64_t out_
 ap_status launch_exchange(const DeviceInfo& di, const Options& o, const float* in, float* out, int64_t groups, int cs,
                           int64_t chunk_bytes, int64_t shift, bool a2a, cudaStream_t stream);
 
+// Launch attribute of kernels that call ptx::wait_previous_grid: their set-up
+// overlaps the end of the grid in front of them.
+inline cudaLaunchAttribute early_start() {
+    cudaLaunchAttribute a{};
+    a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    a.val.programmaticStreamSerializationAllowed = 1;
+    return a;
+}
+
 // Arguments of the 8-bit block-scaled operators as the entry points
 // (fp8_api.cu) have checked them; byte-sized pointers where the element type
 // is a run-time choice.

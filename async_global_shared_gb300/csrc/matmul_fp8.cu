@@ -21,10 +21,10 @@
 //
 // Roles in a CTA, each a warp: the producer streams the operands' 128-byte
 // wide boxes through a ring of shared-memory stages (tensor maps, 128-byte
-// swizzle, rows and columns past the matrix arrive as zeros); a thread a
-// consumer group issues its matrix instructions; a warp brings the scales of
-// the next blocks to shared memory; four consumer warps a group own 32 rows
-// each, one row a thread and up to 128 columns.
+// swizzle, rows and columns past the matrix arrive as zeros); one or two threads
+// issue the matrix instructions; a warp brings the scales of
+// the next blocks to shared memory; consumer warps own 32 rows each, one row
+// a thread and up to 128 columns.
 #include <algorithm>
 #include <atomic>
 
@@ -58,29 +58,33 @@ struct MatmulParams {
     uint32_t* status;
 };
 
-template <int BN, int CG, int STAGES, bool PER_COL>
+template <int BN, int CG, int STAGES, bool PER_COL, bool SWAP>
 struct Form {
-    static constexpr int kGroups = BN > 128 ? 2 : 1;  // consumer groups, side by side along the columns
-    static constexpr int kCols = BN / kGroups;        // columns of a group, and of one matrix instruction
+    static constexpr int kGroups = BN >= 128 ? 2 : 1;    // consumer groups, side by side along the columns
+    static constexpr int kCols = BN / kGroups;           // columns of a group
+    static constexpr int kMmaGroups = BN > 128 ? 2 : 1;  // matrix instructions side by side
+    static constexpr int kMmaCols = BN / kMmaGroups;     // columns of one
     static constexpr int kConsumerWarps = 4 * kGroups;
     static constexpr int kThreads = 32 * (kConsumerWarps + 4);
-    // Two groups: 384 threads of 168 registers at launch (64512), shared out
+    // The widest form: 384 threads of 168 registers at launch (64512), shared out
     // anew: 128 sums and the loads under way need more than 168. With scales
     // by column, 16 columns a load are what fits without spills.
     static constexpr int kOtherRegs = PER_COL ? 56 : 72, kConsumerRegs = PER_COL ? 224 : 216;
     static_assert(128 * kOtherRegs + 256 * kConsumerRegs <= 384 * 168, "registers of the launch");
-    static constexpr int kLoad = kCols < 32 || PER_COL ? 16 : 32;
-    static constexpr int kQBox = kCols / CG;  // rows of Q this CTA loads for a group
+    static constexpr int kLoad = BN <= 64 || PER_COL ? 16 : 32;
+    static constexpr int kQBox = kMmaCols / CG;  // rows of Q this CTA loads for one instruction
     static constexpr uint32_t kPBytes = kTile * kTile, kQBytes = kQBox * kTile;
-    static constexpr uint32_t kStageBytes = kPBytes + kGroups * kQBytes;
-    // Accumulators in flight: a block's products wait in tensor memory from
-    // the matrix instructions' start until a consumer has read them, so the
-    // tensor core is kept busy when its 512 columns cover that time.
-    static constexpr int kBuffers = BN > 128 ? 2 : 4;
-    static constexpr uint32_t kTmemUsed = kBuffers * BN;
-    static constexpr uint32_t kTmemCols = kTmemUsed <= 64 ? 64 : (kTmemUsed <= 128 ? 128 : (kTmemUsed <= 256 ? 256 : 512));
+    static constexpr uint32_t kStageBytes = kPBytes + kMmaGroups * kQBytes;
+    // Accumulators: the products of kRun blocks of k side by side are handed
+    // over at once (a hand-over costs hundreds of cycles whatever its size),
+    // in two buffers. The widest form fills tensor memory with one block each.
+    static constexpr int kRun = BN > 128 ? 1 : (BN > 32 ? 2 : 4);
+    static constexpr int kBuffers = 2;
+    static constexpr uint32_t kTmemCols = kBuffers * kRun * BN;
+    // CTAs an SM: the narrow forms wait more than they compute
+    static constexpr int kCtas = BN > 64 ? 1 : 2;
     // c leaves through shared memory: 4 KiB a consumer warp, 32 rows of 128 bytes
-    static constexpr uint32_t kStagingBytes = kCols >= 64 ? 4096 * kConsumerWarps : 0;
+    static constexpr uint32_t kStagingBytes = SWAP ? 0 : 4096 * kConsumerWarps;
     static constexpr size_t kRingBytes = size_t(STAGES) * kStageBytes;
     static constexpr size_t kSmem = kRingBytes + kStagingBytes + 1024;
     // a split tile's shares: rows of BN floats, padded so that the 32 rows a
@@ -96,7 +100,7 @@ struct __align__(16) Shared {
     float row_scales[kScaleSlots][kScaleRun][kTile + 4];
     float col_scales[kScaleSlots][kScaleRun][PER_COL ? F::kGroups * F::kCols + 4 : 4];  // or one a group
     uint64_t full[STAGES], empty[STAGES];
-    uint64_t acc_full[F::kBuffers][F::kGroups], acc_empty[F::kBuffers][F::kGroups];
+    uint64_t acc_full[F::kBuffers][F::kMmaGroups], acc_empty[F::kBuffers][F::kMmaGroups];
     uint64_t scales_full[kScaleSlots], scales_empty[kScaleSlots];
     uint32_t tmem;
     int abort;
@@ -135,10 +139,11 @@ __device__ __forceinline__ void st_shared4(uint32_t addr, uint4 v) {
 }
 
 template <typename C, int BN, int CG, int STAGES, bool PER_COL, bool SWAP>
-__global__ void __launch_bounds__(Form<BN, CG, STAGES, PER_COL>::kThreads, 1)
+__global__ void __launch_bounds__(Form<BN, CG, STAGES, PER_COL, SWAP>::kThreads, Form<BN, CG, STAGES, PER_COL, SWAP>::kCtas)
     matmul_fp8_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
                       const __grid_constant__ CUtensorMap map_c, const __grid_constant__ MatmulParams P) {
-    using F = Form<BN, CG, STAGES, PER_COL>;
+    using F = Form<BN, CG, STAGES, PER_COL, SWAP>;
+    ptx::let_next_grid_start();
     constexpr int kCols = F::kCols;
     extern __shared__ unsigned char smem_raw[];
     __shared__ Shared<F, STAGES, PER_COL> sh;
@@ -147,8 +152,8 @@ __global__ void __launch_bounds__(Form<BN, CG, STAGES, PER_COL>::kThreads, 1)
     volatile int* abort_flag = &sh.abort;
     const uint32_t rank = CG == 2 || P.split > 1 ? ptx::cluster_ctarank() : 0;
     const int part = CG == 2 ? 0 : static_cast<int>(rank);  // share of k
-    const int32_t kb0 = static_cast<int32_t>(static_cast<int64_t>(P.nkb) * part / P.split);
-    const int32_t kb1 = static_cast<int32_t>(static_cast<int64_t>(P.nkb) * (part + 1) / P.split);
+    const int32_t kb0 = static_cast<uint32_t>(P.nkb * part) / P.split;  // nkb < 2^24, part < 8
+    const int32_t kb1 = static_cast<uint32_t>(P.nkb * (part + 1)) / P.split;
     const int32_t tiles = P.tiles_p * P.tiles_q;  // at most kMaxTiles
     const int32_t per_tile = CG == 2 ? 2 : P.split;  // CTAs of a cluster
     const int32_t first_tile = static_cast<int32_t>(blockIdx.x) / per_tile;
@@ -157,12 +162,12 @@ __global__ void __launch_bounds__(Form<BN, CG, STAGES, PER_COL>::kThreads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             ptx::mbar_init(ptx::smem_addr(&sh.full[s]), 1);
-            ptx::mbar_init(ptx::smem_addr(&sh.empty[s]), F::kGroups);
+            ptx::mbar_init(ptx::smem_addr(&sh.empty[s]), F::kMmaGroups);
         }
-        for (int g = 0; g < F::kGroups; ++g) {
+        for (int g = 0; g < F::kMmaGroups; ++g) {
             for (int s = 0; s < F::kBuffers; ++s) {
                 ptx::mbar_init(ptx::smem_addr(&sh.acc_full[s][g]), 1);
-                ptx::mbar_init(ptx::smem_addr(&sh.acc_empty[s][g]), CG * 4);
+                ptx::mbar_init(ptx::smem_addr(&sh.acc_empty[s][g]), CG * F::kConsumerWarps / F::kMmaGroups);
             }
         }
         for (int s = 0; s < kScaleSlots; ++s) {
@@ -172,12 +177,17 @@ __global__ void __launch_bounds__(Form<BN, CG, STAGES, PER_COL>::kThreads, 1)
         sh.abort = 0;
         ptx::fence_mbar_init();
     }
+    if (threadIdx.x == 32) {
+        ptx::prefetch_tensormap(&map_p);
+        ptx::prefetch_tensormap(&map_q);
+    }
     if (warp == F::kConsumerWarps + 1) ptx::tmem_alloc<CG>(ptx::smem_addr(&sh.tmem), F::kTmemCols);
     ptx::tcgen05_fence_before();
     __syncthreads();
     if (CG == 2) ptx::cluster_sync();  // the other CTA's barriers are ready too
     ptx::tcgen05_fence_after();
     const uint32_t tmem = sh.tmem;
+    ptx::wait_previous_grid();  // nothing above touches global memory
 
     // A wait that gives up ends its role; the CTA's abort flag ends the
     // others. The first probes go without wait_phase's clock reads.
@@ -198,7 +208,7 @@ __global__ void __launch_bounds__(Form<BN, CG, STAGES, PER_COL>::kThreads, 1)
     };
 
     if (warp >= F::kConsumerWarps) {
-        if (F::kGroups == 2) ptx::regs_less<F::kOtherRegs>();
+        if (BN > 128) ptx::regs_less<F::kOtherRegs>();
         if (warp == F::kConsumerWarps) {
             if (ptx::elect_one()) {  // producer
                 uint32_t it = 0;
@@ -222,8 +232,8 @@ __global__ void __launch_bounds__(Form<BN, CG, STAGES, PER_COL>::kThreads, 1)
                         const uint32_t dst = ring + s * F::kStageBytes;
                         ptx::operand_g2s<CG>(dst, &map_p, kb * kTile, p0, bar);
 #pragma unroll
-                        for (int g = 0; g < F::kGroups; ++g)
-                            ptx::operand_g2s<CG>(dst + F::kPBytes + g * F::kQBytes, &map_q, kb * kTile, q0 + g * kCols, bar);
+                        for (int g = 0; g < F::kMmaGroups; ++g)
+                            ptx::operand_g2s<CG>(dst + F::kPBytes + g * F::kQBytes, &map_q, kb * kTile, q0 + g * F::kMmaCols, bar);
                         const uint32_t next = it + 1;
                         ready = next < STAGES || ptx::mbar_test(ptx::smem_addr(&sh.empty[next % STAGES]), (next / STAGES - 1) & 1);
                     }
@@ -236,31 +246,43 @@ __global__ void __launch_bounds__(Form<BN, CG, STAGES, PER_COL>::kThreads, 1)
                                            SITE_MM_DRAIN, abort_flag))
                         break;
             }
-        } else if (warp - F::kConsumerWarps - 1 < F::kGroups) {
-            // Matrix instructions, a warp a group: a block's accumulator and
+        } else if (warp - F::kConsumerWarps - 1 < F::kMmaGroups) {
+            // Matrix instructions, a warp for each of those side by side: a block's accumulator and
             // stage barriers cost one thread more than the instructions take.
             const int g = warp - F::kConsumerWarps - 1;
             if ((CG == 1 || rank == 0) && ptx::elect_one()) {
-                constexpr uint32_t idesc = ptx::e4m3_instr_desc(CG * kTile, kCols);
-                uint32_t it = 0;
+                constexpr uint32_t idesc = ptx::e4m3_instr_desc(CG * kTile, F::kMmaCols);
+                uint32_t it = 0, step = 0;
                 bool ok = true;
                 for (int32_t t = first_tile; t < tiles && ok; t += tile_step) {
-                    for (int32_t kb = kb0; kb < kb1; ++kb, ++it) {
-                        const uint32_t s = it % STAGES, buf = it % F::kBuffers, turn = it / F::kBuffers;
-                        if ((turn > 0 && !wait(&sh.acc_empty[buf][g], (turn - 1) & 1, SITE_MM_MMA_ACC)) ||
-                            !wait(&sh.full[s], (it / STAGES) & 1, SITE_MM_MMA_FULL)) {
+                    for (int32_t kb = kb0; kb < kb1 && ok; ++step) {
+                        const uint32_t buf = step % F::kBuffers, turn = step / F::kBuffers;
+                        // both barriers are asked at once: an answer takes
+                        // over 150 cycles
+                        bool full = ptx::mbar_test(ptx::smem_addr(&sh.full[it % STAGES]), (it / STAGES) & 1);
+                        if (turn > 0 && !wait(&sh.acc_empty[buf][g], (turn - 1) & 1, SITE_MM_MMA_ACC)) {
                             ok = false;
                             break;
                         }
-                        ptx::tcgen05_fence_after();
-                        const uint64_t dp = ptx::operand_desc(ring + s * F::kStageBytes);
-                        const uint64_t dq = ptx::operand_desc(ring + s * F::kStageBytes + F::kPBytes + g * F::kQBytes);
+#pragma unroll 1
+                        for (int j = 0; j < F::kRun && kb < kb1; ++j, ++kb, ++it) {
+                            const uint32_t s = it % STAGES;
+                            if (!full && !wait(&sh.full[s], (it / STAGES) & 1, SITE_MM_MMA_FULL)) {
+                                ok = false;
+                                break;
+                            }
+                            if (j + 1 < F::kRun)
+                                full = ptx::mbar_test(ptx::smem_addr(&sh.full[(it + 1) % STAGES]), ((it + 1) / STAGES) & 1);
+                            ptx::tcgen05_fence_after();
+                            const uint64_t dp = ptx::operand_desc(ring + s * F::kStageBytes);
+                            const uint64_t dq = ptx::operand_desc(ring + s * F::kStageBytes + F::kPBytes + g * F::kQBytes);
 #pragma unroll
-                        for (int k = 0; k < kTile / kMmaK; ++k)
-                            ptx::mma_e4m3<CG>(tmem + (buf * F::kGroups + g) * kCols, dp + k * (kMmaK >> 4),
-                                              dq + k * (kMmaK >> 4), idesc, k > 0);
-                        ptx::mma_commit<CG>(ptx::smem_addr(&sh.acc_full[buf][g]));
-                        ptx::mma_commit<CG>(ptx::smem_addr(&sh.empty[s]));
+                            for (int k = 0; k < kTile / kMmaK; ++k)
+                                ptx::mma_e4m3<CG>(tmem + (buf * F::kRun + j) * BN + g * F::kMmaCols,
+                                                  dp + k * (kMmaK >> 4), dq + k * (kMmaK >> 4), idesc, k > 0);
+                            ptx::mma_commit<CG>(ptx::smem_addr(&sh.empty[s]));
+                        }
+                        if (ok) ptx::mma_commit<CG>(ptx::smem_addr(&sh.acc_full[buf][g]));
                     }
                 }
             }
@@ -306,13 +328,14 @@ __global__ void __launch_bounds__(Form<BN, CG, STAGES, PER_COL>::kThreads, 1)
             ptx::cp_async_wait_all();
         }
     } else {  // consumers
-        if (F::kGroups == 2) ptx::regs_more<F::kConsumerRegs>();
+        if (BN > 128) ptx::regs_more<F::kConsumerRegs>();
         constexpr int kLoad = F::kLoad;  // columns of one load from tensor memory
         constexpr int kLoads = kCols / kLoad;
         const int group = warp / 4, quad = warp % 4;
+        const int source = group * F::kMmaGroups / F::kGroups;  // the matrix instructions whose columns these are
         const int my_row = 32 * quad + lane;  // accumulator row of this thread, in the CTA's 128
         const uint32_t staging = ring + static_cast<uint32_t>(F::kRingBytes) + 4096u * warp;
-        uint32_t it = 0, run = 0;
+        uint32_t step = 0, run = 0;
         bool ok = true;
         for (int32_t t = first_tile; t < tiles; t += tile_step) {
             int32_t tp, tq;
@@ -321,61 +344,75 @@ __global__ void __launch_bounds__(Form<BN, CG, STAGES, PER_COL>::kThreads, 1)
 #pragma unroll
             for (int j = 0; j < kCols; ++j) acc[j] = 0.0f;
             // A warp takes the blocks one after another, so what it waits for
-            // is taken off that path: the next block's barrier is asked before
-            // this block's sums, the next load from tensor memory (the next
-            // block's first one included) is under way while the sums of the
-            // current one are taken, and nothing on the path branches by lane.
+            // is taken off that path: the next accumulator's barrier is asked
+            // before this one's last sums, the next load from tensor memory
+            // (the next block's first one included) is under way while the
+            // sums of the current one are taken, and nothing on the path
+            // branches by lane.
             float v[2][kLoad];
             const uint32_t lanes = tmem + group * kCols + (static_cast<uint32_t>(32 * quad) << 16);
-            ok = ok && warp_wait(&sh.acc_full[it % F::kBuffers][group], (it / F::kBuffers) & 1, SITE_MM_CONSUMER_ACC);
+            ok = ok && warp_wait(&sh.acc_full[step % F::kBuffers][source], (step / F::kBuffers) & 1, SITE_MM_CONSUMER_ACC);
             ok = ok && warp_wait(&sh.scales_full[run % kScaleSlots], (run / kScaleSlots) & 1, SITE_MM_SCALES_FULL);
             if (ok) {
                 ptx::tcgen05_fence_after();
-                ptx::tmem_ld(lanes + (it % F::kBuffers) * BN, v[0]);
+                ptx::tmem_ld(lanes + (step % F::kBuffers) * F::kRun * BN, v[0]);
             }
-            for (int32_t kb = kb0; kb < kb1 && ok; ++kb, ++it) {
-                const uint32_t buf = it % F::kBuffers, slot = run % kScaleSlots;
-                const uint32_t next = it + 1, next_buf = next % F::kBuffers;
+            int j = 0;  // block of the accumulator
+            for (int32_t kb = kb0; kb < kb1 && ok; ++kb) {
+                const uint32_t buf = step % F::kBuffers, slot = run % kScaleSlots;
+                const uint32_t next = step + 1, next_buf = next % F::kBuffers;
                 const int e = (kb - kb0) % kScaleRun;
                 const bool last = kb + 1 == kb1;
-                bool ready = ptx::mbar_test(ptx::smem_addr(&sh.acc_full[next_buf][group]), (next / F::kBuffers) & 1);
+                const bool over = F::kRun == 1 || j == F::kRun - 1 || last;  // the accumulator's last block
+                bool ready = false;
+                if (over)  // (after the last block the answer is not used)
+                    ready = ptx::mbar_test(ptx::smem_addr(&sh.acc_full[next_buf][source]), (next / F::kBuffers) & 1);
                 float scale = sh.row_scales[slot][e][my_row];
                 if (!PER_COL) scale *= sh.col_scales[slot][e][group];
+                const uint32_t at = lanes + (buf * F::kRun + j) * BN;
+                const uint32_t after = over ? lanes + next_buf * F::kRun * BN : at + BN;  // the next block's columns
 #pragma unroll
                 for (int g = 0; g < kLoads; ++g) {
                     ptx::tmem_wait_ld(v[g % 2]);
                     if (g + 1 < kLoads) {
-                        ptx::tmem_ld(lanes + buf * BN + kLoad * (g + 1), v[(g + 1) % 2]);
+                        ptx::tmem_ld(at + kLoad * (g + 1), v[(g + 1) % 2]);
                     } else {
-                        // all of the accumulator is in registers: it is free
-                        // before the last sums are taken
-                        ptx::tcgen05_fence_before();
-                        __syncwarp();
-                        const uint32_t bar = ptx::smem_addr(&sh.acc_empty[buf][group]);
-                        ptx::mbar_arrive_if<CG == 2>(lane == 0, CG == 2 ? ptx::mapa(bar, 0) : bar);
-                        if (!last) {
-                            if (!ready) ready = wait(&sh.acc_full[next_buf][group], (next / F::kBuffers) & 1, SITE_MM_CONSUMER_ACC);
-                            ok = __all_sync(0xffffffffu, ready);
-                            ptx::tcgen05_fence_after();
-                            if (ok && kLoads % 2 == 0) ptx::tmem_ld(lanes + next_buf * BN, v[0]);
+                        if (over) {
+                            // all of the accumulator is in registers: it is
+                            // free before the last sums are taken
+                            ptx::tcgen05_fence_before();
+                            __syncwarp();
+                            const uint32_t bar = ptx::smem_addr(&sh.acc_empty[buf][source]);
+                            ptx::mbar_arrive_if<CG == 2>(lane == 0, CG == 2 ? ptx::mapa(bar, 0) : bar);
+                            if (!last) {
+                                if (!ready)
+                                    ready = wait(&sh.acc_full[next_buf][source], (next / F::kBuffers) & 1, SITE_MM_CONSUMER_ACC);
+                                ok = __all_sync(0xffffffffu, ready);
+                                ptx::tcgen05_fence_after();
+                                if (ok && kLoads % 2 == 0) ptx::tmem_ld(after, v[0]);
+                            }
+                        } else if (kLoads % 2 == 0) {
+                            ptx::tmem_ld(after, v[0]);
                         }
                     }
 #pragma unroll
                     for (int i = 0; i < kLoad; i += 4) {
-                        const int j = kLoad * g + i;
+                        const int col = kLoad * g + i;
                         float4 cs = make_float4(scale, scale, scale, scale);
                         if (PER_COL) {
-                            cs = *reinterpret_cast<const float4*>(&sh.col_scales[slot][e][PER_COL ? group * kCols + j : 0]);
+                            cs = *reinterpret_cast<const float4*>(&sh.col_scales[slot][e][PER_COL ? group * kCols + col : 0]);
                             cs.x *= scale, cs.y *= scale, cs.z *= scale, cs.w *= scale;
                         }
-                        acc[j] = fmaf(v[g % 2][i], cs.x, acc[j]);
-                        acc[j + 1] = fmaf(v[g % 2][i + 1], cs.y, acc[j + 1]);
-                        acc[j + 2] = fmaf(v[g % 2][i + 2], cs.z, acc[j + 2]);
-                        acc[j + 3] = fmaf(v[g % 2][i + 3], cs.w, acc[j + 3]);
+                        acc[col] = fmaf(v[g % 2][i], cs.x, acc[col]);
+                        acc[col + 1] = fmaf(v[g % 2][i + 1], cs.y, acc[col + 1]);
+                        acc[col + 2] = fmaf(v[g % 2][i + 2], cs.z, acc[col + 2]);
+                        acc[col + 3] = fmaf(v[g % 2][i + 3], cs.w, acc[col + 3]);
                     }
                 }
                 // one load a block: its registers are free only now
-                if (kLoads % 2 != 0 && ok && !last) ptx::tmem_ld(lanes + next_buf * BN, v[0]);
+                if (kLoads % 2 != 0 && ok && !last) ptx::tmem_ld(after, v[0]);
+                if (F::kRun > 1) j = over ? 0 : j + 1;
+                step += over ? 1 : 0;
                 if (e == kScaleRun - 1 || last) {  // this run's scales have been read
                     __syncwarp();
                     ptx::mbar_arrive_if<false>(lane == 0, ptx::smem_addr(&sh.scales_empty[slot]));
@@ -396,7 +433,8 @@ __global__ void __launch_bounds__(Form<BN, CG, STAGES, PER_COL>::kThreads, 1)
                     const int col = group * kCols + j;
                     if (SWAP) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) st_shared(ring + 4 * ((col + i) * kTile + my_row), acc[j + i]);
+                        for (int i = 0; i < 4; ++i)
+                            if (q0 + col + i < P.nq) st_shared(ring + 4 * ((col + i) * kTile + my_row), acc[j + i]);
                     } else {
                         st_shared4(ring + 4 * (my_row * F::kSharePitch + col), as_words(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]));
                     }
@@ -463,34 +501,40 @@ __global__ void __launch_bounds__(Form<BN, CG, STAGES, PER_COL>::kThreads, 1)
             int32_t tp, tq;
             tile_at(P, first_tile, &tp, &tq);
             const int64_t p0 = static_cast<int64_t>(tp) * kTile, q0 = static_cast<int64_t>(tq) * BN;
-            if (SWAP) {  // columns of this rank: a thread a row
-                const int c0 = BN * part / P.split, c1 = BN * (part + 1) / P.split;
-                const int my_row = threadIdx.x & 127;
-                for (int c = c0 + (threadIdx.x >> 7); c < c1; c += F::kGroups) {
-                    float v = 0.0f;
-                    for (int r = 0; r < P.split; ++r) v += ptx::cluster_ld(ptx::mapa(ring + 4 * (c * kTile + my_row), r));
-                    if (p0 + my_row < P.np && q0 + c < P.nq)
-                        static_cast<C*>(P.c)[(q0 + c) * P.ldc + p0 + my_row] = from_f32<C>(v);
-                }
-            } else {  // rows of this rank: a warp a row, four columns a lane
-                const int r0 = kTile * part / P.split, r1 = kTile * (part + 1) / P.split;
-                for (int i = r0 + warp; i < r1 && p0 + i < P.np; i += F::kConsumerWarps) {
-                    for (int c = 4 * lane; c < BN; c += 128) {
-                        float4 v = make_float4(0, 0, 0, 0);
-                        for (int r = 0; r < P.split; ++r) {
-                            const float4 w = ptx::cluster_ld4(ptx::mapa(ring + 4 * (i * F::kSharePitch + c), r));
-                            v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
-                        }
-                        C* out = static_cast<C*>(P.c) + (p0 + i) * P.ldc + q0 + c;
-                        const int64_t left = P.nq - q0 - c;
-                        if (P.vec_c && left >= 4) {
-                            store4(out, v);
-                        } else {
-                            const float u[4] = {v.x, v.y, v.z, v.w};
+            const int cols = static_cast<int>(P.nq - q0 < BN ? P.nq - q0 : BN);
+            const int rows = static_cast<int>(P.np - p0 < kTile ? P.np - p0 : kTile);
+            if (SWAP) {  // a thread a value, neighbours of one row of c side by side
+                const int all = cols * kTile;
+                for (int i = all * part / P.split + threadIdx.x; i < all * (part + 1) / P.split; i += 32 * F::kConsumerWarps) {
+                    float w[kMaxSplit];
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                if (e < left) out[e] = from_f32<C>(u[e]);
-                        }
+                    for (int r = 0; r < kMaxSplit; ++r) w[r] = r < P.split ? ptx::cluster_ld(ptx::mapa(ring + 4 * i, r)) : 0.0f;
+                    float v = w[0];
+#pragma unroll
+                    for (int r = 1; r < kMaxSplit; ++r) v += w[r];
+                    const int row = i % kTile, c = i / kTile;
+                    if (row < rows) static_cast<C*>(P.c)[(q0 + c) * P.ldc + p0 + row] = from_f32<C>(v);
+                }
+            } else {  // four values a thread, 16 or 32 neighbouring threads a row
+                constexpr int kQuads = BN / 4;
+                const int all = rows * kQuads;
+                for (int i = all * part / P.split + threadIdx.x; i < all * (part + 1) / P.split; i += 32 * F::kConsumerWarps) {
+                    const int row = i / kQuads, c = i % kQuads * 4;
+                    float4 v = make_float4(0, 0, 0, 0);
+#pragma unroll
+                    for (int r = 0; r < kMaxSplit; ++r) {
+                        if (r >= P.split) break;
+                        const float4 w = ptx::cluster_ld4(ptx::mapa(ring + 4 * (row * F::kSharePitch + c), r));
+                        v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+                    }
+                    C* out = static_cast<C*>(P.c) + (p0 + row) * P.ldc + q0 + c;
+                    if (P.vec_c && c + 4 <= cols) {
+                        store4(out, v);
+                    } else {
+                        const float u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (c + e < cols) out[e] = from_f32<C>(u[e]);
                     }
                 }
             }
@@ -512,10 +556,57 @@ bool box_map(CUtensorMap* map, CUtensorMapDataType type, const void* p, int64_t 
                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Launch configuration of a form's grid in clusters.
+struct Launch {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[2];
+    Launch(int64_t grid, int threads, size_t smem, int cluster, cudaStream_t stream) {
+        cfg.gridDim = dim3(static_cast<unsigned>(grid));
+        cfg.blockDim = dim3(static_cast<unsigned>(threads));
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = stream;
+        attr[0] = early_start();
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = cluster > 1 ? 2 : 1;
+    }
+};
+
+// CTAs of a cluster that share a tile's k: as many (up to 8, each with at
+// least two blocks of k) as leave every tile's cluster resident at once. The
+// SMs of a GPC bound that: one-CTA-an-SM clusters of 4 and 6 leave 144 and 138
+// of the 152 SMs usable, 7 and 8 only 105 and 120. (128 x 2048 x 8192, 16
+// tiles: 24.4 us unsplit, 14.5 split 6, 20.3 split 8 in two waves.)
+// The occupancy call counts one CTA an SM for kernels that use tensor memory;
+// `ctas` is what their tensor memory, registers and shared memory allow.
+template <typename K>
+int split_for(K kernel, int threads, size_t smem, int ctas, std::atomic<int> (&resident)[kMaxSplit + 1], int64_t tiles,
+              int64_t nkb) {
+    for (int split = static_cast<int>(std::min<int64_t>(kMaxSplit, nkb / 2)); split > 1; --split) {
+        int n = resident[split].load();
+        if (n == 0) {
+            Launch l(split, threads, smem, split, nullptr);
+            int per_sm = 0;
+            if (cudaOccupancyMaxActiveClusters(&n, kernel, &l.cfg) != cudaSuccess ||
+                cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) != cudaSuccess || per_sm < 1)
+                n = 0;
+            else if (per_sm < ctas)
+                n = n * ctas / per_sm;
+            n += 1;  // 0: not asked yet
+            resident[split] = n;
+        }
+        if (tiles <= n - 1) return split;
+    }
+    return 1;
+}
+
 template <typename C, int BN, int CG, int STAGES, bool PER_COL, bool SWAP>
-ap_status launch_form(const DeviceInfo& di, MatmulParams P, const MatmulArgs& a, int split, cudaStream_t stream) {
-    using F = Form<BN, CG, STAGES, PER_COL>;
-    static_assert(F::kSmem + sizeof(Shared<F, STAGES, PER_COL>) <= kSmemOptinGB300, "shared memory of a CTA");
+ap_status launch_form(const DeviceInfo& di, MatmulParams P, const MatmulArgs& a, cudaStream_t stream) {
+    using F = Form<BN, CG, STAGES, PER_COL, SWAP>;
+    static_assert(F::kCtas * (F::kSmem + sizeof(Shared<F, STAGES, PER_COL>) + 1024) <= kSmemPerSM, "shared memory of an SM");
+    static_assert(F::kCtas * F::kTmemCols <= 512, "tensor memory of an SM");
     static_assert(CG == 2 || F::kShareBytes <= F::kRingBytes, "a share fits in the ring");
     P.np = SWAP ? a.n : a.m;
     P.nq = SWAP ? a.m : a.n;
@@ -523,20 +614,13 @@ ap_status launch_form(const DeviceInfo& di, MatmulParams P, const MatmulArgs& a,
     P.q_scales = SWAP ? a.a_scales : a.b_scales;
     P.p_shift = SWAP && a.b_block_rows != 1 ? 7 : 0;
     const int64_t tiles_p = (P.np + CG * kTile - 1) / (CG * kTile), tiles_q = (P.nq + BN - 1) / BN;
+    const int64_t tiles = tiles_p * tiles_q;
+    if (tiles > kMaxTiles) return AP_ERR_SHAPE;
     P.tiles_p = static_cast<int32_t>(tiles_p);
     P.tiles_q = static_cast<int32_t>(tiles_q);
-    P.split = split;
-    CUtensorMap mp, mq, mc{};
-    constexpr auto codes = CU_TENSOR_MAP_DATA_TYPE_UINT8;
-    if (!box_map(&mp, codes, SWAP ? a.b : a.a, 1, P.np, a.k, SWAP ? a.ldb : a.lda, kTile) ||
-        !box_map(&mq, codes, SWAP ? a.a : a.b, 1, P.nq, a.k, SWAP ? a.lda : a.ldb, F::kQBox))
-        return AP_ERR_CUDA;
-    if (!SWAP && split == 1 && P.vec_c &&
-        !box_map(&mc, sizeof(C) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, a.c, sizeof(C), a.m,
-                 a.n, a.ldc, 32))
-        return AP_ERR_CUDA;
     auto kernel = matmul_fp8_kernel<C, BN, CG, STAGES, PER_COL, SWAP>;
     static std::atomic<int> configured[64];  // attribute set on this device (setting twice is harmless)
+    static std::atomic<int> resident[64][kMaxSplit + 1];
     if (di.device < 0 || di.device >= 64) return AP_ERR_CUDA;
     if (!configured[di.device].load()) {
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(F::kSmem)) !=
@@ -544,51 +628,37 @@ ap_status launch_form(const DeviceInfo& di, MatmulParams P, const MatmulArgs& a,
             return AP_ERR_CUDA;
         configured[di.device] = 1;
     }
-    const int64_t tiles = tiles_p * tiles_q;
-    if (tiles > kMaxTiles) return AP_ERR_SHAPE;
-    const int cluster = CG == 2 ? 2 : split;
+    P.split = CG == 2 ? 1 : split_for(kernel, F::kThreads, F::kSmem, F::kCtas, resident[di.device], tiles, P.nkb);
+    CUtensorMap mp, mq, mc{};
+    constexpr auto codes = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    if (!box_map(&mp, codes, SWAP ? a.b : a.a, 1, P.np, a.k, SWAP ? a.ldb : a.lda, kTile) ||
+        !box_map(&mq, codes, SWAP ? a.a : a.b, 1, P.nq, a.k, SWAP ? a.lda : a.ldb, F::kQBox))
+        return AP_ERR_CUDA;
+    if (!SWAP && P.split == 1 && P.vec_c &&
+        !box_map(&mc, sizeof(C) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, a.c, sizeof(C), a.m,
+                 a.n, a.ldc, 32))
+        return AP_ERR_CUDA;
+    const int cluster = CG == 2 ? 2 : P.split;
     int64_t grid = tiles * cluster;
-    if (split == 1) grid = std::min<int64_t>(grid, di.sms / cluster * cluster);
-    record_launch(PATH_MATMUL, grid, BN, static_cast<int64_t>(F::kSmem), STAGES, (SWAP ? 1 : 0) | (CG == 2 ? 2 : 0) | split << 4);
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid));
-    cfg.blockDim = dim3(F::kThreads);
-    cfg.dynamicSmemBytes = F::kSmem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = cluster > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, mp, mq, mc, P) == cudaSuccess ? AP_OK : AP_ERR_CUDA;
-}
-
-// CTAs of a cluster that share a tile's k: as many as keep the SMs busy, each
-// with at least two blocks of k.
-int split_for(const DeviceInfo& di, int64_t tiles, int64_t nkb) {
-    int split = 1;
-    while (split < kMaxSplit && tiles * split * 2 <= di.sms && nkb >= 4 * split) split *= 2;
-    return split;
+    if (P.split == 1) grid = std::min<int64_t>(grid, di.sms * F::kCtas / cluster * cluster);
+    record_launch(PATH_MATMUL, grid, BN, static_cast<int64_t>(F::kSmem), STAGES,
+                  (SWAP ? 1 : 0) | (CG == 2 ? 2 : 0) | P.split << 4);
+    Launch l(grid, F::kThreads, F::kSmem, cluster, stream);
+    return cudaLaunchKernelEx(&l.cfg, kernel, mp, mq, mc, P) == cudaSuccess ? AP_OK : AP_ERR_CUDA;
 }
 
 template <typename C>
 ap_status launch_mm(const DeviceInfo& di, const MatmulParams& P, const MatmulArgs& a, cudaStream_t stream) {
-    const auto tiles_of = [&](int64_t pr, int64_t p, int64_t qr, int64_t q) { return (pr + p - 1) / p * ((qr + q - 1) / q); };
     const bool rows = a.b_block_rows == 1;
-    if (a.m <= 64) {
-        const int64_t bn = a.m <= 16 ? 16 : (a.m <= 32 ? 32 : 64);
-        const int split = split_for(di, tiles_of(a.n, kTile, a.m, bn), P.nkb);
-        if (a.m <= 16) return launch_form<C, 16, 1, 10, true, true>(di, P, a, split, stream);
-        if (a.m <= 32) return launch_form<C, 32, 1, 9, true, true>(di, P, a, split, stream);
-        return launch_form<C, 64, 1, 7, true, true>(di, P, a, split, stream);
-    }
-    if (tiles_of(a.m, 2 * kTile, a.n, 256) >= di.sms / 4)
-        return rows ? launch_form<C, 256, 2, 5, true, false>(di, P, a, 1, stream)
-                    : launch_form<C, 256, 2, 5, false, false>(di, P, a, 1, stream);
-    const int split = split_for(di, tiles_of(a.m, kTile, a.n, kTile), P.nkb);
-    return rows ? launch_form<C, 128, 1, 5, true, false>(di, P, a, split, stream)
-                : launch_form<C, 128, 1, 5, false, false>(di, P, a, split, stream);
+    if (a.m <= 16) return launch_form<C, 16, 1, 5, true, true>(di, P, a, stream);
+    if (a.m <= 32) return launch_form<C, 32, 1, 4, true, true>(di, P, a, stream);
+    if (a.m <= 64) return launch_form<C, 64, 1, 4, true, true>(di, P, a, stream);
+    const int64_t pairs = (a.m + 2 * kTile - 1) / (2 * kTile) * ((a.n + 255) / 256);
+    if (pairs >= di.sms / 4)
+        return rows ? launch_form<C, 256, 2, 5, true, false>(di, P, a, stream)
+                    : launch_form<C, 256, 2, 5, false, false>(di, P, a, stream);
+    return rows ? launch_form<C, 128, 1, 5, true, false>(di, P, a, stream)
+                : launch_form<C, 128, 1, 5, false, false>(di, P, a, stream);
 }
 
 }  // namespace

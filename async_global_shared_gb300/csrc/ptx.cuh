@@ -256,6 +256,15 @@ __device__ __forceinline__ void cluster_sync() {
             : "memory");
 }
 
+// ---------------------------------------------------------------- consecutive grids
+
+// A grid launched with early_start (internal.h) may begin before the grid in
+// front of it in the stream has ended. It touches no global memory before
+// wait_previous_grid, which every thread executes; let_next_grid_start lets
+// the grid behind it do the same.
+__device__ __forceinline__ void let_next_grid_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_previous_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ---------------------------------------------------------------- misc
 
 __device__ __forceinline__ uint64_t globaltimer_ns() {
