@@ -347,15 +347,14 @@ def ap_debug_scale_pages_async(inp, out, n_tiles: int, tile_elems: int, alpha: f
 
 
 # ------------------------------------------------------------------ 8-bit block-scaled operators
+#
+# These calls are made once a layer and token, so their checks are written for
+# few attribute look-ups: one look at a tensor's device, shape, strides, type
+# and address each.
 
 SCALE_BLOCK = 128  # values of a row that share a scale
 
-
-def _blocks(n: int) -> int:
-    return -(-n // SCALE_BLOCK)
-
-
-_DTYPES = None  # torch dtype -> ap_dtype, and the dtypes that hold e4m3 codes
+_DTYPES = None  # torch dtype -> ap_dtype; the dtypes that hold e4m3 codes; the current device's number; float32
 
 
 def _dtypes():
@@ -364,61 +363,76 @@ def _dtypes():
         import torch
 
         _DTYPES = ({torch.float32: AP_F32, torch.bfloat16: AP_BF16, torch.float16: AP_F16},
-                   (torch.float8_e4m3fn, torch.uint8), torch._C._cuda_getDevice)
+                   (torch.float8_e4m3fn, torch.uint8), torch._C._cuda_getDevice, torch.float32)
     return _DTYPES
 
 
-def _on_device(t, name: str):
-    if not t.is_cuda or t.get_device() != _dtypes()[2]():
+def _device(t, name: str) -> int:
+    """The device of a call's first tensor, which must be the current one."""
+    dev = t.get_device()  # -1 for a host tensor
+    if dev < 0 or dev != _dtypes()[2]():
+        raise TypeError(f"{name} must be a tensor on the current CUDA device")
+    return dev
+
+
+def _where(t, name: str, dev: int):
+    if t.get_device() != dev:
         raise TypeError(f"{name} must be a tensor on the current CUDA device")
 
 
 def _kind(t, name: str) -> int:
-    kind = _dtypes()[0].get(t.dtype)
+    kind = _DTYPES[0].get(t.dtype)
     if kind is None:
         raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
     return kind
 
 
-def _matrix(t, name: str, shape=None) -> int:
-    """Leading dimension of a 2-D tensor with unit column stride, on the current device."""
-    _on_device(t, name)
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
-        raise ValueError(f"{name} must be a matrix{'' if shape is None else ' of shape %s' % (tuple(shape),)}, got {tuple(t.shape)}")
-    rows, cols = t.shape
-    row_stride, col_stride = t.stride()
-    if cols > 1 and col_stride != 1:
-        raise ValueError(f"{name} must have a column stride of 1")
+def _matrix(t, name: str, shape, dev: int) -> int:
+    """Leading dimension of a matrix of this shape with unit column stride, on this device."""
+    if t.get_device() != dev:
+        raise TypeError(f"{name} must be a tensor on the current CUDA device")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be a matrix of shape {tuple(shape)}, got {tuple(t.shape)}")
+    rows, cols = shape
+    ld, col_stride = t.stride()
     if rows <= 1:
         # a single row's stride is never used: give one its columns fit in and
         # that the 16-byte rule of the products accepts
-        return -(-cols // 16) * 16
-    if row_stride < cols:
+        ld = -(-cols // 16) * 16
+    elif ld < cols:
         raise ValueError(f"{name} must have rows that do not overlap")
-    return row_stride
+    if col_stride != 1 and cols > 1:
+        raise ValueError(f"{name} must have a column stride of 1")
+    return ld
 
 
-def _codes(t, name: str, shape) -> int:
-    if t.dtype not in _dtypes()[1]:
+def _codes(t, name: str, shape, dev: int) -> int:
+    if t.dtype not in _DTYPES[1]:
         raise TypeError(f"{name} must be float8_e4m3fn (or uint8 codes), got {t.dtype}")
-    return _matrix(t, name, shape)
+    return _matrix(t, name, shape, dev)
 
 
-def _floats(t, name: str, shape):
+def _floats(t, name: str, shape, dev: int) -> int:
     """Address of a contiguous float32 tensor of this shape."""
-    import torch
-
-    _on_device(t, name)
-    if t.dtype != torch.float32 or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+    if t.get_device() != dev:
+        raise TypeError(f"{name} must be a tensor on the current CUDA device")
+    if t.dtype != _DTYPES[3] or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous float32 tensor of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
     return t.data_ptr()
 
 
-def _weight(t, cols: int) -> int:
-    _on_device(t, "weight")
-    if tuple(t.shape) != (cols,) or not t.is_contiguous():
+def _weight(t, cols: int, dev: int) -> int:
+    _where(t, "weight", dev)
+    if t.shape != (cols,) or not t.is_contiguous():
         raise ValueError(f"weight must be a contiguous vector of {cols}, got {tuple(t.shape)}")
     return _kind(t, "weight")
+
+
+def _shape2(t, name: str):
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be a matrix, got {tuple(shape)}")
+    return shape
 
 
 def ap_rms_norm(x, weight, eps: float, y=None, q=None, q_scales=None, residual=None, residual_out=None, rstd=None,
@@ -428,38 +442,49 @@ def ap_rms_norm(x, weight, eps: float, y=None, q=None, q_scales=None, residual=N
     ``y``: the output in x's type; ``q`` (float8_e4m3fn or uint8) and ``q_scales`` (float32, rows x ceil(cols / 128)):
     the output in 8 bits. ``residual`` and ``residual_out`` (the same tensor for in place) are of x's type or float32
     and share a row stride; ``rstd`` receives r, which the gradient needs."""
-    ldx = _matrix(x, "x")
-    shape = x.shape
+    dev = _device(x, "x")
+    shape = _shape2(x, "x")
     rows, cols = shape
-    ldr = ldy = ldq = cols
+    ldx = _matrix(x, "x", shape, dev)
     rtype = kind = _kind(x, "x")
+    res = out = yp = qp = sp = rp = None
+    ldr = ldy = ldq = cols
     if residual is not None:
-        ldr = _matrix(residual, "residual", shape)
-        rtype = _kind(residual, "residual")
         if residual_out is None:
             raise ValueError("residual needs residual_out (the same tensor for in place)")
-    if residual_out is not None:
-        if residual is None or residual_out.dtype != residual.dtype or _matrix(residual_out, "residual_out", shape) != ldr:
-            raise ValueError("residual_out must match residual in type and row stride")
+        ldr = _matrix(residual, "residual", shape, dev)
+        rtype = _kind(residual, "residual")
+        res = out = residual.data_ptr()
+        if residual_out is not residual:
+            if residual_out.dtype != residual.dtype or _matrix(residual_out, "residual_out", shape, dev) != ldr:
+                raise ValueError("residual_out must match residual in type and row stride")
+            out = residual_out.data_ptr()
+    elif residual_out is not None:
+        raise ValueError("residual_out needs residual")
     if y is not None:
-        ldy = _matrix(y, "y", shape)
+        ldy = _matrix(y, "y", shape, dev)
         if y.dtype != x.dtype:
             raise TypeError("y must have x's type")
+        yp = y.data_ptr()
     if q is not None:
-        ldq = _codes(q, "q", shape)
         if q_scales is None:
             raise ValueError("q needs q_scales")
-    _check(load().ap_rms_norm(
-        x.data_ptr(), ldx, kind, None if residual is None else residual.data_ptr(),
-        None if residual_out is None else residual_out.data_ptr(), ldr, rtype, weight.data_ptr(), _weight(weight, cols),
-        eps, rows, cols, None if y is None else y.data_ptr(), ldy, None if q is None else q.data_ptr(), ldq,
-        None if q_scales is None else _floats(q_scales, "q_scales", (rows, _blocks(cols))),
-        None if rstd is None else _floats(rstd, "rstd", (rows,)), _stream(stream)), "ap_rms_norm")
+        ldq = _codes(q, "q", shape, dev)
+        qp = q.data_ptr()
+    if q_scales is not None:
+        sp = _floats(q_scales, "q_scales", (rows, (cols + 127) // 128), dev)
+    if rstd is not None:
+        rp = _floats(rstd, "rstd", (rows,), dev)
+    wtype = _weight(weight, cols, dev)
+    status = (_lib or load()).ap_rms_norm(x.data_ptr(), ldx, kind, res, out, ldr, rtype, weight.data_ptr(), wtype, eps, rows,
+                                          cols, yp, ldy, qp, ldq, sp, rp, _stream(stream))
+    if status:
+        raise APError(status, "ap_rms_norm")
 
 
 def ap_rms_norm_backward_workspace(rows: int, cols: int) -> int:
     """Bytes of workspace ap_rms_norm_backward needs for these sizes."""
-    size = load().ap_rms_norm_backward_workspace(rows, cols)
+    size = (_lib or load()).ap_rms_norm_backward_workspace(rows, cols)
     if size < 0:
         raise APError(2, "ap_rms_norm_backward_workspace")
     return size
@@ -471,27 +496,34 @@ def ap_rms_norm_backward(dy, h, weight, rstd, dx, dweight=None, workspace=None, 
     ``h``: the forward call's residual_out, or its x where there was no residual; ``dresidual``: a gradient of h from
     elsewhere, added to dx; ``workspace``: a contiguous uint8 tensor of at least ap_rms_norm_backward_workspace(rows,
     cols) bytes, needed with dweight."""
-    lddy = _matrix(dy, "dy")
-    shape = dy.shape
+    dev = _device(dy, "dy")
+    shape = _shape2(dy, "dy")
     rows, cols = shape
-    ldh, lddx = _matrix(h, "h", shape), _matrix(dx, "dx", shape)
-    lddr = cols
+    lddy, ldh, lddx = _matrix(dy, "dy", shape, dev), _matrix(h, "h", shape, dev), _matrix(dx, "dx", shape, dev)
+    kind, rtype = _kind(dy, "dy"), _kind(h, "h")
     if dx.dtype != h.dtype:
         raise TypeError("dx must have h's type")
+    dp = wp = sp = None
+    lddr = cols
     if dresidual is not None:
-        lddr = _matrix(dresidual, "dresidual", shape)
+        lddr = _matrix(dresidual, "dresidual", shape, dev)
         if dresidual.dtype != h.dtype:
             raise TypeError("dresidual must have h's type")
+        dp = dresidual.data_ptr()
+    if dweight is not None:
+        wp = _floats(dweight, "dweight", (cols,), dev)
     if workspace is not None:
-        _on_device(workspace, "workspace")
-        have = workspace.numel() * workspace.element_size()
-        if not workspace.is_contiguous() or (dweight is not None and have < ap_rms_norm_backward_workspace(rows, cols)):
+        _where(workspace, "workspace", dev)
+        if not workspace.is_contiguous() or (
+                wp is not None and workspace.nbytes < ap_rms_norm_backward_workspace(rows, cols)):
             raise ValueError(f"workspace must be contiguous, of at least {ap_rms_norm_backward_workspace(rows, cols)} bytes")
-    _check(load().ap_rms_norm_backward(
-        dy.data_ptr(), lddy, _kind(dy, "dy"), h.data_ptr(), ldh, _kind(h, "h"), weight.data_ptr(), _weight(weight, cols),
-        _floats(rstd, "rstd", (rows,)), None if dresidual is None else dresidual.data_ptr(), lddr, rows, cols,
-        dx.data_ptr(), lddx, None if dweight is None else _floats(dweight, "dweight", (cols,)),
-        None if workspace is None else workspace.data_ptr(), _stream(stream)), "ap_rms_norm_backward")
+        sp = workspace.data_ptr()
+    wtype = _weight(weight, cols, dev)
+    status = (_lib or load()).ap_rms_norm_backward(
+        dy.data_ptr(), lddy, kind, h.data_ptr(), ldh, rtype, weight.data_ptr(), wtype, _floats(rstd, "rstd", (rows,), dev), dp,
+        lddr, rows, cols, dx.data_ptr(), lddx, wp, sp, _stream(stream))
+    if status:
+        raise APError(status, "ap_rms_norm_backward")
 
 
 def ap_quantize(x, block_rows: int, q=None, scales=None, qt=None, scales_t=None, stream=None):
@@ -499,35 +531,49 @@ def ap_quantize(x, block_rows: int, q=None, scales=None, qt=None, scales_t=None,
 
     ``block_rows`` 1: a scale for 128 consecutive values of a row of the output (scales rows x ceil(cols / 128),
     scales_t cols x ceil(rows / 128)); 128: a scale for each 128 x 128 tile."""
-    ldx = _matrix(x, "x")
-    rows, cols = x.shape
+    dev = _device(x, "x")
+    shape = _shape2(x, "x")
+    rows, cols = shape
+    ldx = _matrix(x, "x", shape, dev)
+    kind = _kind(x, "x")
+    tile = block_rows if block_rows == 1 or block_rows == 128 else 1  # other values are the library's to refuse
     ldq, ldqt = cols, rows
-    tile = block_rows if block_rows in (1, SCALE_BLOCK) else 1  # other values are the library's to refuse
+    qp = sp = qtp = stp = None
     if q is not None:
-        ldq = _codes(q, "q", (rows, cols))
         if scales is None:
             raise ValueError("q needs scales")
+        ldq = _codes(q, "q", shape, dev)
+        qp = q.data_ptr()
+    if scales is not None:
+        sp = _floats(scales, "scales", ((rows + tile - 1) // tile, (cols + 127) // 128), dev)
     if qt is not None:
-        ldqt = _codes(qt, "qt", (cols, rows))
         if scales_t is None:
             raise ValueError("qt needs scales_t")
-    _check(load().ap_quantize(
-        x.data_ptr(), ldx, _kind(x, "x"), rows, cols, block_rows, None if q is None else q.data_ptr(), ldq,
-        None if scales is None else _floats(scales, "scales", (-(-rows // tile), _blocks(cols))),
-        None if qt is None else qt.data_ptr(), ldqt,
-        None if scales_t is None else _floats(scales_t, "scales_t", (-(-cols // tile), _blocks(rows))),
-        _stream(stream)), "ap_quantize")
+        ldqt = _codes(qt, "qt", (cols, rows), dev)
+        qtp = qt.data_ptr()
+    if scales_t is not None:
+        stp = _floats(scales_t, "scales_t", ((cols + tile - 1) // tile, (rows + 127) // 128), dev)
+    status = (_lib or load()).ap_quantize(x.data_ptr(), ldx, kind, rows, cols, block_rows, qp, ldq, sp, qtp, ldqt, stp,
+                                          _stream(stream))
+    if status:
+        raise APError(status, "ap_quantize")
 
 
 def ap_matmul_fp8(a, a_scales, b, b_scales, c, b_block_rows: int = SCALE_BLOCK, stream=None):
     """c = a * b^T of e4m3 matrices: a (m x k) scaled by row blocks, b (n x k) by 128 x 128 tiles (``b_block_rows`` 128)
     or by row blocks (1), c (m x n) float32, bfloat16 or float16. Rows of a and b start on 16-byte boundaries."""
-    lda, ldb, ldc = _codes(a, "a", a.shape), _codes(b, "b", b.shape), _matrix(c, "c")
-    (m, k), (n, kb) = a.shape, b.shape
-    if k != kb or tuple(c.shape) != (m, n):
-        raise ValueError(f"shapes do not match: a {tuple(a.shape)}, b {tuple(b.shape)}, c {tuple(c.shape)}")
-    tile = b_block_rows if b_block_rows in (1, SCALE_BLOCK) else 1
-    _check(load().ap_matmul_fp8(
-        a.data_ptr(), lda, _floats(a_scales, "a_scales", (m, _blocks(k))), b.data_ptr(), ldb,
-        _floats(b_scales, "b_scales", (-(-n // tile), _blocks(k))), b_block_rows, c.data_ptr(), ldc, _kind(c, "c"),
-        m, n, k, _stream(stream)), "ap_matmul_fp8")
+    dev = _device(a, "a")
+    m, k = _shape2(a, "a")
+    n, kb = _shape2(b, "b")
+    if k != kb:
+        raise ValueError(f"shapes do not match: a {tuple(a.shape)}, b {tuple(b.shape)}")
+    lda, ldb, ldc = _codes(a, "a", a.shape, dev), _codes(b, "b", b.shape, dev), _matrix(c, "c", (m, n), dev)
+    kind = _kind(c, "c")
+    tile = b_block_rows if b_block_rows == 1 or b_block_rows == 128 else 1
+    blocks = (k + 127) // 128
+    status = (_lib or load()).ap_matmul_fp8(
+        a.data_ptr(), lda, _floats(a_scales, "a_scales", (m, blocks), dev), b.data_ptr(), ldb,
+        _floats(b_scales, "b_scales", ((n + tile - 1) // tile, blocks), dev), b_block_rows, c.data_ptr(), ldc, kind, m, n, k,
+        _stream(stream))
+    if status:
+        raise APError(status, "ap_matmul_fp8")

@@ -23,7 +23,7 @@ OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libasyncpipe.so")
 
 SOURCES = ["api.cu", "stream_ring.cu", "roll_small.cu", "scale_sync.cu", "exchange.cu", "fma_probe.cu", "masked_copy.cu", "autotune.cu", "fp8_api.cu",
-           "rms_norm.cu", "quantize.cu", "matmul_fp8.cu"]
+           "rms_norm.cu", "rms_norm_grad.cu", "quantize.cu", "matmul_fp8.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

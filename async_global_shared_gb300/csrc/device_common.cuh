@@ -34,6 +34,9 @@ enum WaitSite : uint32_t {
     SITE_MM_DRAIN = 17,
     SITE_MM_SCALES_EMPTY = 18,
     SITE_MM_SCALES_FULL = 19,
+    SITE_ROWS_PRODUCER = 20,
+    SITE_ROWS_CONSUMER = 21,
+    SITE_ROWS_DRAIN = 22,
 };
 
 constexpr uint32_t kStatusTimeout = 9;  // AP_ERR_DEVICE_TIMEOUT

@@ -91,7 +91,7 @@ ap_status ap_rms_norm(const void* x, int64_t ldx, ap_dtype type, const void* res
     if (st != AP_OK) return st;
     NormArgs a{x, residual, residual_out, weight, y, q, q_scales, rstd, rows, cols, ldx, ldr, ldy, ldq, type, residual_type,
                weight_type, eps};
-    return launch_rms_norm(di, a, stream);
+    return launch_rms_norm(di, options(), a, stream);
 }
 
 int64_t ap_rms_norm_backward_workspace(int64_t rows, int64_t cols) {
@@ -146,7 +146,7 @@ ap_status ap_rms_norm_backward(const void* dy, int64_t lddy, ap_dtype type, cons
     if (st != AP_OK) return st;
     NormGradArgs a{dy, h, weight, rstd, dresidual, dx, dweight, static_cast<float*>(workspace), rows, cols, lddy, ldh,
                    lddr, lddx, type, residual_type, weight_type};
-    return launch_rms_norm_backward(di, a, stream);
+    return launch_rms_norm_backward(di, options(), a, stream);
 }
 
 ap_status ap_quantize(const void* x, int64_t ldx, ap_dtype type, int64_t rows, int64_t cols, int block_rows, uint8_t* q,

@@ -77,20 +77,25 @@ struct Raw8<float> {
     }
 };
 
+// The whole chunk at p, 16-byte aligned.
+template <typename T>
+__device__ __forceinline__ Raw8<T> load8(const T* p) {
+    Raw8<T> r;
+    if constexpr (sizeof(T) == 4) {
+        r.a = *reinterpret_cast<const float4*>(p);
+        r.b = *reinterpret_cast<const float4*>(p + 4);
+    } else {
+        r.w = *reinterpret_cast<const uint4*>(p);
+    }
+    return r;
+}
+
 // The chunk at p: the first `n` of eight elements, zeros after them (n <= 0:
 // nothing is read). vec: p is 16-byte aligned.
 template <typename T>
 __device__ __forceinline__ Raw8<T> load8(const T* p, bool vec, int64_t n) {
+    if (vec && n >= 8) return load8(p);
     Raw8<T> r;
-    if (vec && n >= 8) {
-        if constexpr (sizeof(T) == 4) {
-            r.a = *reinterpret_cast<const float4*>(p);
-            r.b = *reinterpret_cast<const float4*>(p + 4);
-        } else {
-            r.w = *reinterpret_cast<const uint4*>(p);
-        }
-        return r;
-    }
     if constexpr (sizeof(T) == 4) {
         float v[8];
 #pragma unroll
@@ -110,17 +115,23 @@ __device__ __forceinline__ Raw8<T> load8(const T* p, bool vec, int64_t n) {
     return r;
 }
 
+// Store eight values at p, 16-byte aligned.
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float (&v)[8]) {
+    if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+        *reinterpret_cast<uint4*>(p) =
+            make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7]));
+    }
+}
+
 // Store the first `n` of eight values. vec: p is 16-byte aligned.
 template <typename T>
 __device__ __forceinline__ void store8(T* p, bool vec, int64_t n, const float (&v)[8]) {
     if (vec && n >= 8) {
-        if constexpr (sizeof(T) == 4) {
-            *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-            *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
-        } else {
-            *reinterpret_cast<uint4*>(p) =
-                make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7]));
-        }
+        store8(p, v);
         return;
     }
 #pragma unroll
@@ -146,14 +157,37 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return r;
 }
 
-__device__ __forceinline__ float amax8(const float (&v)[8]) {
-    float m = fabsf(v[0]);
-#pragma unroll
-    for (int i = 1; i < 8; ++i) m = max_nan(m, fabsf(v[i]));
-    return m;
+// The largest magnitude of three values, NaN if any is.
+__device__ __forceinline__ float amax3(float a, float b, float c) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 
-__device__ __forceinline__ float scale_of(float amax) { return max_nan(__fdiv_rn(amax, kE4m3Max), kMinScale); }
+__device__ __forceinline__ float amax8(const float (&v)[8]) {
+    return amax3(amax3(v[0], v[1], v[2]), amax3(v[3], v[4], v[5]), amax3(v[6], v[7], 0.0f));
+}
+
+// A block's scale s = max(amax / 448, 2^-126) and 1 / s, both rounded to
+// nearest. Every half warp of the norm and the quantiser computes them once a
+// chunk, so they are written without the branches of the general operations:
+// the quotient by a constant is Markstein's (the product with the rounded
+// reciprocal, then one step with the exact remainder), the reciprocal one
+// Newton step on the hardware's approximation. Both agree with division and
+// reciprocal for every mantissa; s is never below the normal range, and an
+// infinite amax, whose remainder would be NaN, has its own answer.
+struct Scale {
+    float s, inv;
+};
+__device__ __forceinline__ Scale scale_of(float amax) {
+    constexpr float kRecip = 1.0f / kE4m3Max;
+    const bool infinite = amax > 3.402823466e38f;
+    const float q = amax * kRecip;
+    const float s = max_nan(fmaf(fmaf(-kE4m3Max, q, amax), kRecip, q), kMinScale);
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(s));
+    return Scale{infinite ? amax : s, infinite ? 0.0f : fmaf(y, fmaf(-s, y, 1.0f), y)};
+}
 
 // Two e4m3 codes, a in the lower byte. The magnitudes are at most 448 but for
 // the rounding of the product, which the saturation absorbs; NaN stays NaN.

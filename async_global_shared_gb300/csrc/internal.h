@@ -149,6 +149,19 @@ inline cudaLaunchAttribute early_start() {
     return a;
 }
 
+// Launch of such a kernel without dynamic shared memory or clusters.
+template <typename... Args>
+ap_status launch_early(void (*kernel)(Args...), int64_t grid, int threads, cudaStream_t stream, const Args&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.stream = stream;
+    cudaLaunchAttribute attr = early_start();
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? AP_OK : AP_ERR_CUDA;
+}
+
 // Arguments of the 8-bit block-scaled operators as the entry points
 // (fp8_api.cu) have checked them; byte-sized pointers where the element type
 // is a run-time choice.
@@ -165,7 +178,7 @@ struct NormArgs {
     ap_dtype type, residual_type, weight_type;
     float eps;
 };
-ap_status launch_rms_norm(const DeviceInfo& di, const NormArgs& a, cudaStream_t stream);
+ap_status launch_rms_norm(const DeviceInfo& di, const Options& o, const NormArgs& a, cudaStream_t stream);
 
 struct NormGradArgs {
     const void* dy;
@@ -179,8 +192,9 @@ struct NormGradArgs {
     int64_t rows, cols, lddy, ldh, lddr, lddx;
     ap_dtype type, residual_type, weight_type;
 };
-ap_status launch_rms_norm_backward(const DeviceInfo& di, const NormGradArgs& a, cudaStream_t stream);
-// Rows of partial sums (cols floats each) the launcher above writes.
+ap_status launch_rms_norm_backward(const DeviceInfo& di, const Options& o, const NormGradArgs& a,
+                                   cudaStream_t stream);
+// Rows of partial sums (cols floats each) the launcher above writes at most.
 int64_t norm_grad_partials(int64_t rows, int64_t cols);
 
 struct QuantArgs {

@@ -28,6 +28,8 @@ __device__ __forceinline__ float half_warp_max(float m) {
 // Row blocks only: a half warp a block, no exchange beyond its shuffles.
 template <typename T>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const __grid_constant__ QuantParams P) {
+    ptx::let_next_grid_start();
+    ptx::wait_previous_grid();
     const QuantArgs& a = P.a;
     const int64_t block = static_cast<int64_t>(blockIdx.x) * 16 + threadIdx.x / 16;
     const int64_t row = block / P.blocks, bj = block % P.blocks;
@@ -35,9 +37,9 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const __grid_constan
     const int64_t n = row < a.rows ? a.cols - col : 0;
     float v[8];
     load8(static_cast<const T*>(a.x) + row * a.ldx + col, P.vec_x, n).unpack(v);
-    const float s = scale_of(half_warp_max(amax8(v)));
-    if (n > 0) store_codes(a.q + row * a.ldq + col, P.vec_q, n, codes8(v, __frcp_rn(s)));
-    if (n > 0 && (threadIdx.x & 15) == 0) a.scales[block] = s;
+    const Scale s = scale_of(half_warp_max(amax8(v)));
+    if (n > 0) store_codes(a.q + row * a.ldq + col, P.vec_q, n, codes8(v, s.inv));
+    if (n > 0 && (threadIdx.x & 15) == 0) a.scales[block] = s.s;
 }
 
 // A 128 x 128 tile a CTA: thread t holds rows 8 (t / 16) .. + 7 of columns
@@ -46,6 +48,8 @@ template <typename T>
 __global__ void __launch_bounds__(256) quantize_tile_kernel(const __grid_constant__ QuantParams P) {
     __shared__ float col_max[8][kScaleBlock];  // per warp, or [w][0]: the warp's amax (tiles)
     __shared__ __align__(16) uint2 turned[kScaleBlock][16];  // [column][8-row unit, exchanged by the column's chunk]
+    ptx::let_next_grid_start();
+    ptx::wait_previous_grid();
     const QuantArgs& a = P.a;
     const int chunk = threadIdx.x & 15, rows8 = threadIdx.x >> 4, warp = threadIdx.x >> 5;
     const int64_t tj = blockIdx.x % P.blocks, ti = blockIdx.x / P.blocks;
@@ -73,11 +77,11 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(const __grid_constan
         m = col_max[0][0];
 #pragma unroll
         for (int w = 1; w < 8; ++w) m = max_nan(m, col_max[w][0]);
-        const float s = scale_of(m);
-        inv_tile = __frcp_rn(s);
+        const Scale s = scale_of(m);
+        inv_tile = s.inv;
         if (threadIdx.x == 0) {
-            if (a.q != nullptr) a.scales[ti * P.blocks + tj] = s;
-            if (a.qt != nullptr) a.scales_t[tj * P.blocks_t + ti] = s;
+            if (a.q != nullptr) a.scales[ti * P.blocks + tj] = s.s;
+            if (a.qt != nullptr) a.scales_t[tj * P.blocks_t + ti] = s.s;
         }
     } else if (a.qt != nullptr) {
         float m[8] = {0, 0, 0, 0, 0, 0, 0, 0};
@@ -98,10 +102,10 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(const __grid_constan
             float c = col_max[0][threadIdx.x];
 #pragma unroll
             for (int w = 1; w < 8; ++w) c = max_nan(c, col_max[w][threadIdx.x]);
-            const float s = scale_of(c);
+            const Scale s = scale_of(c);
             const int64_t j = tj * kScaleBlock + threadIdx.x;
-            if (j < a.cols) a.scales_t[j * P.blocks_t + ti] = s;
-            col_max[0][threadIdx.x] = __frcp_rn(s);
+            if (j < a.cols) a.scales_t[j * P.blocks_t + ti] = s.s;
+            col_max[0][threadIdx.x] = s.inv;
         }
         __syncthreads();
 #pragma unroll
@@ -114,9 +118,9 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(const __grid_constan
             raw[p].unpack(v);
             float inv = inv_tile;
             if (!tiles) {
-                const float s = scale_of(half_warp_max(amax8(v)));
-                inv = __frcp_rn(s);
-                if (chunk == 0 && row0 + p < a.rows) a.scales[(row0 + p) * P.blocks + tj] = s;
+                const Scale s = scale_of(half_warp_max(amax8(v)));
+                inv = s.inv;
+                if (chunk == 0 && row0 + p < a.rows) a.scales[(row0 + p) * P.blocks + tj] = s.s;
             }
             if (row0 + p < a.rows && col < a.cols)
                 store_codes(a.q + (row0 + p) * a.ldq + col, P.vec_q, a.cols - col, codes8(v, inv));
@@ -167,11 +171,8 @@ ap_status launch_quant_t(const QuantArgs& a, cudaStream_t stream) {
     const int64_t grid = rows_only ? (a.rows * P.blocks + 15) / 16 : P.blocks * P.blocks_t;
     if (grid >= (int64_t(1) << 31)) return AP_ERR_SHAPE;
     record_launch(PATH_QUANTIZE, grid, rows_only ? 8 : 64, 0, 0, 0);
-    if (rows_only)
-        quantize_rows_kernel<T><<<static_cast<unsigned>(grid), 256, 0, stream>>>(P);
-    else
-        quantize_tile_kernel<T><<<static_cast<unsigned>(grid), 256, 0, stream>>>(P);
-    return cudaGetLastError() == cudaSuccess ? AP_OK : AP_ERR_CUDA;
+    return rows_only ? launch_early(quantize_rows_kernel<T>, grid, 256, stream, P)
+                     : launch_early(quantize_tile_kernel<T>, grid, 256, stream, P);
 }
 
 }  // namespace

@@ -1,34 +1,12 @@
 // Root-mean-square norm with the residual's addition and an output in 16/32
-// bits and / or e4m3, and its gradient.
-//
-// Forward, for a row of N values:
+// bits and / or e4m3. For a row of N values:
 //     h = x + residual,  r = 1 / sqrt(sum(h^2) / N + eps),  y = h r w.
-// Backward, with n = h r and g = dy w: r depends on every h of the row,
-// d r / d h_i = -r^3 h_i / N, so
-//     dx = r (g - n mean(g n)) + dresidual,   dw_j = sum over rows of dy n.
-// Both need one sum over the row before the first output, so a row is held
-// in registers between the two and memory is passed over once.
-#include <algorithm>
-
-#include "device_common.cuh"
-#include "fp8_common.cuh"
-#include "internal.h"
+// The sum comes before the first output, so a row is held in registers between
+// the two and memory is passed over once.
+#include "row_ring.cuh"
 
 namespace ap {
 namespace {
-
-// Sum over the threads that hold one row: a warp, or the whole CTA (every
-// warp adds the warps' sums in the same order, so all threads get one value).
-template <bool WARP>
-__device__ __forceinline__ float row_sum(float v, float* scratch) {
-    v = warp_sum(v);
-    if (WARP) return v;
-    const int warps = blockDim.x >> 5;
-    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = (threadIdx.x & 31) < warps ? scratch[threadIdx.x & 31] : 0.0f;
-    return warp_sum(v);
-}
 
 struct NormParams {
     NormArgs a;
@@ -36,28 +14,45 @@ struct NormParams {
     int64_t blocks;                          // scales of a row
 };
 
-template <typename T>
-__device__ __forceinline__ void load_weight(const void* w, bool same, bool vec, int64_t col, int64_t n, float (&v)[8]) {
-    if (same)
-        load8(static_cast<const T*>(w) + col, vec, n).unpack(v);
-    else
-        load8(static_cast<const float*>(w) + col, vec, n).unpack(v);
-}
-
-// y of one chunk and what is written of it. The 16 lanes of a half warp hold
-// one block of 128, so its amax is four shuffles away.
-template <typename T>
-__device__ __forceinline__ void write_chunk(const NormParams& P, int64_t row, int64_t col, int64_t n, const float (&y)[8]) {
+// What is written of a row's y, C chunks a thread `step` columns apart, the
+// first at col. The 16 lanes of a half warp hold one block of 128, so a
+// block's amax is four shuffles away; the chunks' shuffles run side by side.
+// WHOLE: chunks are whole or empty and every output is aligned.
+template <typename T, int C, bool WHOLE>
+__device__ __forceinline__ void write_row(const NormParams& P, int64_t row, int64_t col, int64_t step, const float (&y)[C][8]) {
     const NormArgs& a = P.a;
-    if (a.y != nullptr && n > 0) store8(static_cast<T*>(a.y) + row * a.ldy + col, P.vec_y, n, y);
-    if (a.q != nullptr) {
-        float m = amax8(y);
+    const int64_t left = a.cols - col;
+    if (a.y != nullptr) {
+        T* out = static_cast<T*>(a.y) + (row * a.ldy + col);
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const float s = scale_of(m);
-        if (n > 0) {
-            store_codes(a.q + row * a.ldq + col, P.vec_q, n, codes8(y, __frcp_rn(s)));
-            if ((threadIdx.x & 15) == 0) a.q_scales[row * P.blocks + col / kScaleBlock] = s;
+        for (int c = 0; c < C; ++c) {
+            if (left <= c * step) continue;
+            if (WHOLE)
+                store8(out + c * step, y[c]);
+            else
+                store8(out + c * step, P.vec_y, left - c * step, y[c]);
+        }
+    }
+    if (a.q != nullptr) {
+        uint8_t* out = a.q + (row * a.ldq + col);
+        float* scales = a.q_scales + (row * P.blocks + col / kScaleBlock);
+        float m[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) m[c] = amax8(y[c]);
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+            for (int c = 0; c < C; ++c) m[c] = max_nan(m[c], __shfl_xor_sync(0xffffffffu, m[c], o));
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            if (left <= c * step) continue;
+            const Scale s = scale_of(m[c]);
+            const uint2 w = codes8(y[c], s.inv);
+            if (WHOLE)
+                *reinterpret_cast<uint2*>(out + c * step) = w;
+            else
+                store_codes(out + c * step, P.vec_q, left - c * step, w);
+            if ((threadIdx.x & 15) == 0) scales[c * step / kScaleBlock] = s.s;
         }
     }
 }
@@ -66,6 +61,8 @@ __device__ __forceinline__ void write_chunk(const NormParams& P, int64_t row, in
 template <typename T, typename R, int C, bool WARP>
 __global__ void __launch_bounds__(WARP ? 256 : 1024) rms_norm_kernel(const __grid_constant__ NormParams P) {
     __shared__ float scratch[32];
+    ptx::let_next_grid_start();
+    ptx::wait_previous_grid();
     const NormArgs& a = P.a;
     const int lane = WARP ? threadIdx.x & 31 : threadIdx.x;
     const int width = WARP ? 32 : blockDim.x;
@@ -105,8 +102,109 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) rms_norm_kernel(const __gri
         float w[8];
         load_weight<T>(a.weight, a.weight_type == a.type, P.vec_w, col, a.cols - col, w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] *= h[c][i] * r;
-        write_chunk<T>(P, row, col, a.cols - col, w);
+        for (int i = 0; i < 8; ++i) h[c][i] *= r * w[i];
+    }
+    write_row<T, C, false>(P, row, 8 * lane, 8 * width, h);
+}
+
+// The ring's form: teams of warps, rows from shared memory, the weight in
+// registers for the whole grid's life (four chunks: in shared memory).
+template <typename T, typename R, int C, bool RES, Weights W>
+__global__ void __launch_bounds__(kRingThreads, 1)
+    rms_norm_ring_kernel(const __grid_constant__ NormParams P, const __grid_constant__ RowRing ring) {
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ RingBars bars;
+    __shared__ float scratch[2][kRingWarps];
+    constexpr bool kKeep = W == IN_REGISTERS;
+    ptx::let_next_grid_start();
+    ring_init(ring, bars);
+    const NormArgs& a = P.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp == kRingWarps) {
+        ring_produce(ring, bars, ptx::smem_addr(smem));
+        return;
+    }
+    float* weights = reinterpret_cast<float*>(smem + ring.weight_offset);
+    if (W == IN_SHARED) stage_weights<T>(a.weight, a.weight_type == a.type, a.cols, weights);
+    const int team = warp / ring.team_warps, width = 32 * ring.team_warps;
+    if (team >= ring.teams) return;
+    const int me = threadIdx.x - team * width;
+    const int apart = 8 * width;  // columns between a thread's chunks
+    const int left = static_cast<int>(a.cols) - 8 * me;
+    float w[kKeep ? C : 1][8];
+    if (kKeep) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[kKeep ? c : 0][i] = 0.0f;
+            if (left > c * apart) load_weight<T>(a.weight, a.weight_type == a.type, 8 * me + c * apart, w[kKeep ? c : 0]);
+        }
+    }
+    const float inv = __frcp_rn(static_cast<float>(a.cols));
+    const int64_t step = ring.together * ring.turns;
+    const int groups = ring.teams / ring.together, group = team / ring.together, mate = team % ring.together;
+    int s = group, turn = 0;
+    uint32_t round = 0;
+    while (s >= ring.stages) s -= ring.stages, ++round;
+    for (int64_t base = (blockIdx.x + static_cast<int64_t>(gridDim.x) * group) * step; base < a.rows;
+         base += gridDim.x * groups * step) {
+        bool ok = true;
+        if (lane == 0) ok = ring_wait(ring, bars, &bars.full[s], round & 1, SITE_ROWS_CONSUMER);
+        if (!__shfl_sync(0xffffffffu, static_cast<int>(ok), 0)) break;
+        const unsigned char* stage = smem + s * ring.stage_bytes;
+        for (int m = 0; m < ring.turns; ++m, turn ^= 1) {
+            const int slot = m * ring.together + mate;
+            const int64_t row = base + slot;
+            const bool mine = row < a.rows;  // the same for the whole team
+            float h[C][8];
+            if (mine) {
+                const T* x = reinterpret_cast<const T*>(stage + slot * ring.bytes[0]) + 8 * me;
+                const R* res = reinterpret_cast<const R*>(stage + ring.offset[1] + slot * ring.bytes[1]) + 8 * me;
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) h[c][i] = 0.0f;
+                    if (left <= c * apart) continue;
+                    load8(x + c * apart).unpack(h[c]);
+                    if (RES) {
+                        float v[8];
+                        load8(res + c * apart).unpack(v);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) h[c][i] += v[i];
+                    }
+                }
+            }
+            if (m == ring.turns - 1) {  // everything of the stage is in registers
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&bars.empty[s]));
+            }
+            if (!mine) continue;
+            float sum = 0.0f;
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sum = fmaf(h[c][i], h[c][i], sum);
+            if (RES) {
+                R* out = static_cast<R*>(a.residual_out) + (row * a.ldr + 8 * me);
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+                    if (left > c * apart) store8(out + c * apart, h[c]);
+            }
+            sum = team_sum(sum, &scratch[turn][team * ring.team_warps], team, ring.team_warps);
+            const float r = __frcp_rn(__fsqrt_rn(fmaf(sum, inv, a.eps)));
+            if (a.rstd != nullptr && me == 0) a.rstd[row] = r;
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                float again[8];
+                if (!kKeep && left > c * apart) again_weight<T, W>(P, weights, 8 * me + c * apart, again);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (kKeep || left > c * apart) h[c][i] *= r * (kKeep ? w[kKeep ? c : 0][i] : again[i]);
+            }
+            write_row<T, C, true>(P, row, 8 * me, apart, h);
+        }
+        s += groups;
+        while (s >= ring.stages) s -= ring.stages, ++round;
     }
 }
 
@@ -116,6 +214,8 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) rms_norm_kernel(const __gri
 template <typename T, typename R>
 __global__ void __launch_bounds__(1024) rms_norm_wide_kernel(const __grid_constant__ NormParams P) {
     __shared__ float scratch[32];
+    ptx::let_next_grid_start();
+    ptx::wait_previous_grid();
     const NormArgs& a = P.a;
     const int64_t row = blockIdx.x;
     const T* x = static_cast<const T*>(a.x) + row * a.ldx;
@@ -143,20 +243,16 @@ __global__ void __launch_bounds__(1024) rms_norm_wide_kernel(const __grid_consta
     // whole warps stay in the loop, for the shuffles of a block's amax
     for (int64_t base = 0; base < a.cols; base += step) {
         const int64_t col = base + 8 * static_cast<int64_t>(threadIdx.x);
-        float h[8], w[8];
-        load_h(col, h);
+        float h[1][8], w[8];
+        load_h(col, h[0]);
         if (res != nullptr && col < a.cols)
-            store8(static_cast<R*>(a.residual_out) + row * a.ldr + col, P.vec_r, a.cols - col, h);
+            store8(static_cast<R*>(a.residual_out) + row * a.ldr + col, P.vec_r, a.cols - col, h[0]);
         load_weight<T>(a.weight, a.weight_type == a.type, P.vec_w, col, a.cols - col, w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] *= h[i] * r;
-        write_chunk<T>(P, row, col, a.cols - col, w);
+        for (int i = 0; i < 8; ++i) h[0][i] *= r * w[i];
+        write_row<T, 1, false>(P, row, col, 0, h);
     }
 }
-
-constexpr int64_t kMaxGrid = int64_t(1) << 31;
-
-ap_status launched() { return cudaGetLastError() == cudaSuccess ? AP_OK : AP_ERR_CUDA; }
 
 template <typename T, typename R, int C, bool WARP>
 ap_status launch_norm_c(const NormParams& P, cudaStream_t stream) {
@@ -165,12 +261,31 @@ ap_status launch_norm_c(const NormParams& P, cudaStream_t stream) {
     const int64_t grid = WARP ? (P.a.rows + 7) / 8 : P.a.rows;
     if (grid >= kMaxGrid) return AP_ERR_SHAPE;
     record_launch(PATH_NORM, grid, 8 * C, 0, 0, WARP ? 1 : 0);
-    rms_norm_kernel<T, R, C, WARP><<<static_cast<unsigned>(grid), threads, 0, stream>>>(P);
-    return launched();
+    return launch_early(rms_norm_kernel<T, R, C, WARP>, grid, threads, stream, P);
 }
 
+template <typename T, typename R, bool RES>
+ap_status launch_norm_ring(const DeviceInfo& di, const NormParams& P, const RowRing& ring, cudaStream_t stream) {
+    static std::atomic<int> configured[5][64];
+    if (ring.chunks == 2)
+        return launch_ring_kernel(di, rms_norm_ring_kernel<T, R, 2, RES, IN_REGISTERS>, configured[0], P, ring, PATH_NORM, stream);
+    if (ring.chunks == 3)
+        return ring.keep_weights
+                   ? launch_ring_kernel(di, rms_norm_ring_kernel<T, R, 3, RES, IN_SHARED>, configured[1], P, ring, PATH_NORM, stream)
+                   : launch_ring_kernel(di, rms_norm_ring_kernel<T, R, 3, RES, IN_L2>, configured[2], P, ring, PATH_NORM, stream);
+    return ring.keep_weights
+               ? launch_ring_kernel(di, rms_norm_ring_kernel<T, R, 4, RES, IN_SHARED>, configured[3], P, ring, PATH_NORM, stream)
+               : launch_ring_kernel(di, rms_norm_ring_kernel<T, R, 4, RES, IN_L2>, configured[4], P, ring, PATH_NORM, stream);
+}
+
+// The ring's set-up is paid back from this many elements on (1216 x 4096: 8.2
+// us against 8.8 without, 2432 x 4096: 13.7 against 16.9, 16384 x 4096: 72
+// against 88); short rows are too much work for its one producer (16384 x 256:
+// 9.6 us, 6.3 without).
+constexpr int64_t kRingElements = int64_t(1) << 23, kRingColumns = 1024;
+
 template <typename T, typename R>
-ap_status launch_norm_t(const DeviceInfo&, const NormArgs& a, cudaStream_t stream) {
+ap_status launch_norm_t(const DeviceInfo& di, const Options& o, const NormArgs& a, cudaStream_t stream) {
     NormParams P;
     P.a = a;
     P.vec_x = rows_aligned(a.x, a.ldx, sizeof(T), 16);
@@ -179,205 +294,36 @@ ap_status launch_norm_t(const DeviceInfo&, const NormArgs& a, cudaStream_t strea
     P.vec_q = rows_aligned(a.q, a.ldq, 1, 8);
     P.vec_w = reinterpret_cast<uintptr_t>(a.weight) % 16 == 0;
     P.blocks = (a.cols + kScaleBlock - 1) / kScaleBlock;
+    RowRing ring;
+    const void* const in[] = {a.x, a.residual};
+    const int64_t ld[] = {a.ldx, a.ldr}, size[] = {sizeof(T), sizeof(R)};
+    const bool res = a.residual != nullptr;
+    const bool whole = (!res || P.vec_r) && P.vec_w && (a.y == nullptr || P.vec_y) && (a.q == nullptr || P.vec_q);
+    const bool many = o.force_path == 1 || (o.force_path != 2 && a.cols > kRingColumns && a.rows >= kRingElements / a.cols);
+    if (many && whole && plan_ring(di, o, &ring, res ? 2 : 1, in, ld, size, nullptr, a.rows, a.cols)) {
+        return res ? launch_norm_ring<T, R, true>(di, P, ring, stream) : launch_norm_ring<T, T, false>(di, P, ring, stream);
+    }
     if (a.cols <= 256) return launch_norm_c<T, R, 1, true>(P, stream);
     if (a.cols <= 512) return launch_norm_c<T, R, 2, true>(P, stream);
-    if (a.cols <= 1024) return launch_norm_c<T, R, 4, true>(P, stream);
     if (a.cols <= 4096) return launch_norm_c<T, R, 1, false>(P, stream);
     if (a.cols <= 8192) return launch_norm_c<T, R, 2, false>(P, stream);
     if (a.cols <= 32768) return launch_norm_c<T, R, 4, false>(P, stream);
     if (a.rows >= kMaxGrid) return AP_ERR_SHAPE;
     record_launch(PATH_NORM, a.rows, 0, 0, 0, 2);
-    rms_norm_wide_kernel<T, R><<<static_cast<unsigned>(a.rows), 1024, 0, stream>>>(P);
-    return launched();
-}
-
-// ------------------------------------------------------------------ gradient
-
-struct GradParams {
-    NormGradArgs a;
-    bool vec_dy, vec_h, vec_r, vec_dx, vec_w;
-};
-
-// CTA b takes rows b, b + grid, ...; a thread keeps its columns' share of
-// dweight in registers and writes it to the CTA's row of the workspace at the
-// end, so the sum's order depends on the sizes alone.
-template <typename T, typename R, int C>
-__global__ void __launch_bounds__(512) rms_norm_grad_kernel(const __grid_constant__ GradParams P) {
-    __shared__ float scratch[2][32];
-    const NormGradArgs& a = P.a;
-    float dw[C][8];
-#pragma unroll
-    for (int c = 0; c < C; ++c)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) dw[c][i] = 0.0f;
-    const float inv = __frcp_rn(static_cast<float>(a.cols));
-    int turn = 0;  // two scratch rows in turn: one barrier a row is enough
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
-        const T* dy = static_cast<const T*>(a.dy) + row * a.lddy;
-        const R* h = static_cast<const R*>(a.h) + row * a.ldh;
-        const float r = a.rstd[row];
-        float g[C][8], n[C][8];
-        float sum = 0.0f;
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const int64_t col = 8 * static_cast<int64_t>(c * blockDim.x + threadIdx.x);
-            float w[8];
-            load8(dy + col, P.vec_dy, a.cols - col).unpack(g[c]);
-            load8(h + col, P.vec_h, a.cols - col).unpack(n[c]);
-            load_weight<T>(a.weight, a.weight_type == a.type, P.vec_w, col, a.cols - col, w);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                n[c][i] *= r;
-                dw[c][i] = fmaf(g[c][i], n[c][i], dw[c][i]);
-                g[c][i] *= w[i];
-                sum = fmaf(g[c][i], n[c][i], sum);
-            }
-        }
-        const float mean = row_sum<false>(sum, scratch[turn]) * inv;
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const int64_t col = 8 * static_cast<int64_t>(c * blockDim.x + threadIdx.x);
-            if (col >= a.cols) continue;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) g[c][i] = fmaf(-n[c][i], mean, g[c][i]);
-            float d[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            if (a.dresidual != nullptr)
-                load8(static_cast<const R*>(a.dresidual) + row * a.lddr + col, P.vec_r, a.cols - col).unpack(d);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) g[c][i] = fmaf(r, g[c][i], d[i]);
-            store8(static_cast<R*>(a.dx) + row * a.lddx + col, P.vec_dx, a.cols - col, g[c]);
-        }
-    }
-    if (a.dweight == nullptr) return;
-    float* part = a.workspace + static_cast<int64_t>(blockIdx.x) * a.cols;
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-        const int64_t col = 8 * static_cast<int64_t>(c * blockDim.x + threadIdx.x);
-        if (col < a.cols) store8(part + col, a.cols % 4 == 0, a.cols - col, dw[c]);
-    }
-}
-
-// Rows too wide for registers: two passes over each row, and the CTA's share
-// of dweight is added up in its row of the workspace (every thread its own
-// columns).
-template <typename T, typename R>
-__global__ void __launch_bounds__(1024) rms_norm_grad_wide_kernel(const __grid_constant__ GradParams P) {
-    __shared__ float scratch[2][32];
-    const NormGradArgs& a = P.a;
-    const float inv = __frcp_rn(static_cast<float>(a.cols));
-    int turn = 0;
-    const bool same = a.weight_type == a.type;
-    auto weight = [&](int64_t j) {
-        return same ? to_f32(static_cast<const T*>(a.weight)[j]) : static_cast<const float*>(a.weight)[j];
-    };
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
-        const T* dy = static_cast<const T*>(a.dy) + row * a.lddy;
-        const R* h = static_cast<const R*>(a.h) + row * a.ldh;
-        const float r = a.rstd[row];
-        float sum = 0.0f;
-        for (int64_t j = threadIdx.x; j < a.cols; j += blockDim.x)
-            sum = fmaf(to_f32(dy[j]) * weight(j), to_f32(h[j]) * r, sum);
-        const float mean = row_sum<false>(sum, scratch[turn]) * inv;
-        for (int64_t j = threadIdx.x; j < a.cols; j += blockDim.x) {
-            const float d = to_f32(dy[j]), n = to_f32(h[j]) * r;
-            const float more =
-                a.dresidual != nullptr ? to_f32(static_cast<const R*>(a.dresidual)[row * a.lddr + j]) : 0.0f;
-            static_cast<R*>(a.dx)[row * a.lddx + j] = from_f32<R>(fmaf(r, fmaf(-n, mean, d * weight(j)), more));
-            if (a.dweight != nullptr) {
-                float* part = a.workspace + static_cast<int64_t>(blockIdx.x) * a.cols + j;
-                *part = row == blockIdx.x ? d * n : fmaf(d, n, *part);
-            }
-        }
-    }
-}
-
-// dweight from the CTAs' shares: a CTA sums 32 columns, eight rows of
-// partials at a time, and adds the eight sums in order.
-__global__ void __launch_bounds__(256) sum_partials_kernel(const float* part, float* out, int64_t parts, int64_t cols) {
-    __shared__ float sums[8][32];
-    const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x % 32;
-    const int y = threadIdx.x / 32;
-    float v = 0.0f;
-    if (col < cols)
-        for (int64_t p = y; p < parts; p += 8) v += part[p * cols + col];
-    sums[y][threadIdx.x % 32] = v;
-    __syncthreads();
-    if (y == 0 && col < cols) {
-#pragma unroll
-        for (int i = 1; i < 8; ++i) v += sums[i][threadIdx.x];
-        out[col] = v;
-    }
-}
-
-constexpr int64_t kGradSMs = 152;  // the partials' number is part of the interface (workspace size), so no device query
-
-template <typename T, typename R, int C>
-void run_grad(const GradParams& P, int64_t grid, cudaStream_t stream) {
-    const int64_t chunks = (P.a.cols + 7) / 8;
-    const int threads = static_cast<int>(((chunks + C - 1) / C + 31) / 32 * 32);
-    record_launch(PATH_NORM_GRAD, grid, 8 * C, 0, 0, 0);
-    rms_norm_grad_kernel<T, R, C><<<static_cast<unsigned>(grid), threads, 0, stream>>>(P);
-}
-
-template <typename T, typename R>
-ap_status launch_grad_t(const NormGradArgs& a, cudaStream_t stream) {
-    GradParams P;
-    P.a = a;
-    P.vec_dy = rows_aligned(a.dy, a.lddy, sizeof(T), 16);
-    P.vec_h = rows_aligned(a.h, a.ldh, sizeof(R), 16);
-    P.vec_r = rows_aligned(a.dresidual, a.lddr, sizeof(R), 16);
-    P.vec_dx = rows_aligned(a.dx, a.lddx, sizeof(R), 16);
-    P.vec_w = reinterpret_cast<uintptr_t>(a.weight) % 16 == 0;
-    const int64_t grid = norm_grad_partials(a.rows, a.cols);
-    if (grid > 0) {
-        if (a.cols <= 4096) {
-            run_grad<T, R, 1>(P, grid, stream);
-        } else if (a.cols <= 8192) {
-            run_grad<T, R, 2>(P, grid, stream);
-        } else if (a.cols <= 16384) {
-            run_grad<T, R, 4>(P, grid, stream);
-        } else {
-            record_launch(PATH_NORM_GRAD, grid, 0, 0, 0, 2);
-            rms_norm_grad_wide_kernel<T, R><<<static_cast<unsigned>(grid), 1024, 0, stream>>>(P);
-        }
-        const ap_status st = launched();
-        if (st != AP_OK) return st;
-    }
-    if (a.dweight == nullptr) return AP_OK;
-    sum_partials_kernel<<<static_cast<unsigned>((a.cols + 31) / 32), 256, 0, stream>>>(a.workspace, a.dweight, grid,
-                                                                                      a.cols);
-    return launched();
+    return launch_early(rms_norm_wide_kernel<T, R>, a.rows, 1024, stream, P);
 }
 
 }  // namespace
 
-// CTAs of the gradient's kernel: as many as are resident at once (by their
-// threads), each with at least one row.
-int64_t norm_grad_partials(int64_t rows, int64_t cols) {
-    const int64_t per_sm = cols <= 2048 ? 8 : (cols <= 4096 ? 4 : 2);
-    return std::min(rows, kGradSMs * per_sm);
-}
-
-ap_status launch_rms_norm(const DeviceInfo& di, const NormArgs& a, cudaStream_t stream) {
+ap_status launch_rms_norm(const DeviceInfo& di, const Options& o, const NormArgs& a, cudaStream_t stream) {
     const bool same = a.residual == nullptr || a.residual_type == a.type;
     switch (a.type) {
         case AP_BF16:
-            return same ? launch_norm_t<__nv_bfloat16, __nv_bfloat16>(di, a, stream)
-                        : launch_norm_t<__nv_bfloat16, float>(di, a, stream);
+            return same ? launch_norm_t<__nv_bfloat16, __nv_bfloat16>(di, o, a, stream)
+                        : launch_norm_t<__nv_bfloat16, float>(di, o, a, stream);
         case AP_F16:
-            return same ? launch_norm_t<__half, __half>(di, a, stream) : launch_norm_t<__half, float>(di, a, stream);
-        default: return launch_norm_t<float, float>(di, a, stream);
-    }
-}
-
-ap_status launch_rms_norm_backward(const DeviceInfo&, const NormGradArgs& a, cudaStream_t stream) {
-    const bool same = a.residual_type == a.type;
-    switch (a.type) {
-        case AP_BF16:
-            return same ? launch_grad_t<__nv_bfloat16, __nv_bfloat16>(a, stream)
-                        : launch_grad_t<__nv_bfloat16, float>(a, stream);
-        case AP_F16: return same ? launch_grad_t<__half, __half>(a, stream) : launch_grad_t<__half, float>(a, stream);
-        default: return launch_grad_t<float, float>(a, stream);
+            return same ? launch_norm_t<__half, __half>(di, o, a, stream) : launch_norm_t<__half, float>(di, o, a, stream);
+        default: return launch_norm_t<float, float>(di, o, a, stream);
     }
 }
 

@@ -1,0 +1,340 @@
+// Gradient of the root-mean-square norm. With n = h r and g = dy w: r depends on
+// every h of the row, d r / d h_i = -r^3 h_i / N, so
+//     dx = r (g - n mean(g n)) + dresidual,   dw_j = sum over rows of dy n.
+// The mean comes before the first dx, so a row is held on the chip between the
+// two and memory is passed over once.
+#include "row_ring.cuh"
+
+namespace ap {
+namespace {
+
+struct GradParams {
+    NormGradArgs a;
+    bool vec_dy, vec_h, vec_r, vec_dx, vec_w;
+};
+
+// CTA b takes rows b, b + grid, ...; a thread keeps its columns' share of
+// dweight in registers and writes it to the CTA's row of the workspace at the
+// end, so the sum's order depends on the sizes alone.
+template <typename T, typename R, int C>
+__global__ void __launch_bounds__(512) rms_norm_grad_kernel(const __grid_constant__ GradParams P) {
+    __shared__ float scratch[2][32];
+    ptx::let_next_grid_start();
+    ptx::wait_previous_grid();
+    const NormGradArgs& a = P.a;
+    float dw[C][8];
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dw[c][i] = 0.0f;
+    const float inv = __frcp_rn(static_cast<float>(a.cols));
+    int turn = 0;  // two scratch rows in turn: one barrier a row is enough
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+        const T* dy = static_cast<const T*>(a.dy) + row * a.lddy;
+        const R* h = static_cast<const R*>(a.h) + row * a.ldh;
+        const float r = a.rstd[row];
+        float g[C][8], n[C][8];
+        float sum = 0.0f;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int64_t col = 8 * static_cast<int64_t>(c * blockDim.x + threadIdx.x);
+            float w[8];
+            load8(dy + col, P.vec_dy, a.cols - col).unpack(g[c]);
+            load8(h + col, P.vec_h, a.cols - col).unpack(n[c]);
+            load_weight<T>(a.weight, a.weight_type == a.type, P.vec_w, col, a.cols - col, w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                n[c][i] *= r;
+                dw[c][i] = fmaf(g[c][i], n[c][i], dw[c][i]);
+                g[c][i] *= w[i];
+                sum = fmaf(g[c][i], n[c][i], sum);
+            }
+        }
+        const float mean = row_sum<false>(sum, scratch[turn]) * inv;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int64_t col = 8 * static_cast<int64_t>(c * blockDim.x + threadIdx.x);
+            if (col >= a.cols) continue;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) g[c][i] = fmaf(-n[c][i], mean, g[c][i]);
+            float d[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            if (a.dresidual != nullptr)
+                load8(static_cast<const R*>(a.dresidual) + row * a.lddr + col, P.vec_r, a.cols - col).unpack(d);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) g[c][i] = fmaf(r, g[c][i], d[i]);
+            store8(static_cast<R*>(a.dx) + row * a.lddx + col, P.vec_dx, a.cols - col, g[c]);
+        }
+    }
+    if (a.dweight == nullptr) return;
+    float* part = a.workspace + static_cast<int64_t>(blockIdx.x) * a.cols;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int64_t col = 8 * static_cast<int64_t>(c * blockDim.x + threadIdx.x);
+        if (col < a.cols) store8(part + col, a.cols % 4 == 0, a.cols - col, dw[c]);
+    }
+}
+
+// The ring's form: teams of warps, rows and their rstd from shared memory. A
+// thread's columns are the same for every row, so it keeps their weights (four
+// chunks: in shared memory) and their share of dweight in registers.
+template <typename T, typename R, int C, bool RES, Weights W>
+__global__ void __launch_bounds__(kRingThreads, 1)
+    rms_norm_grad_ring_kernel(const __grid_constant__ GradParams P, const __grid_constant__ RowRing ring) {
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ RingBars bars;
+    __shared__ float scratch[2][kRingWarps];
+    constexpr bool kKeep = W == IN_REGISTERS;
+    ptx::let_next_grid_start();
+    ring_init(ring, bars);
+    const NormGradArgs& a = P.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp == kRingWarps) {
+        ring_produce(ring, bars, ptx::smem_addr(smem));
+        return;
+    }
+    const bool same = a.weight_type == a.type;
+    float* weights = reinterpret_cast<float*>(smem + ring.weight_offset);
+    if (W == IN_SHARED) stage_weights<T>(a.weight, same, a.cols, weights);
+    const int team = warp / ring.team_warps, width = 32 * ring.team_warps;
+    if (team >= ring.teams) return;
+    const int me = threadIdx.x - team * width;
+    const int cols = static_cast<int>(a.cols);  // a multiple of 8
+    float w[kKeep ? C : 1][8];
+    if (kKeep) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int col = 8 * (c * width + me);
+            if (col < cols) load_weight<T>(a.weight, same, col, w[kKeep ? c : 0]);
+        }
+    }
+    float dw[C][8];
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dw[c][i] = 0.0f;
+    const float inv = __frcp_rn(static_cast<float>(a.cols));
+    const int64_t step = ring.together * ring.turns;
+    const int groups = ring.teams / ring.together, group = team / ring.together, mate = team % ring.together;
+    int s = group, turn = 0;
+    uint32_t round = 0;
+    while (s >= ring.stages) s -= ring.stages, ++round;
+    for (int64_t base = (blockIdx.x + static_cast<int64_t>(gridDim.x) * group) * step; base < a.rows;
+         base += gridDim.x * groups * step) {
+        bool ok = true;
+        if (lane == 0) ok = ring_wait(ring, bars, &bars.full[s], round & 1, SITE_ROWS_CONSUMER);
+        if (!__shfl_sync(0xffffffffu, static_cast<int>(ok), 0)) break;
+        const unsigned char* stage = smem + s * ring.stage_bytes;
+        for (int m = 0; m < ring.turns; ++m, turn ^= 1) {
+            const int slot = m * ring.together + mate;
+            const int64_t row = base + slot;
+            const bool mine = row < a.rows;  // the same for the whole team
+            if (mine) {
+                // the row is read from shared memory again after its sum: that
+                // is cheaper than the registers it would take
+                const T* p = reinterpret_cast<const T*>(stage + slot * ring.bytes[0]);
+                const R* q = reinterpret_cast<const R*>(stage + ring.offset[1] + slot * ring.bytes[1]);
+                const float r = reinterpret_cast<const float*>(stage + ring.side_offset)[slot];
+                float sum = 0.0f;
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    const int col = 8 * (c * width + me);
+                    if (col >= cols) continue;
+                    float g[8], n[8], again[8];
+                    load8(p + col).unpack(g);
+                    load8(q + col).unpack(n);
+                    if (!kKeep) again_weight<T, W>(P, weights, col, again);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        n[i] *= r;
+                        dw[c][i] = fmaf(g[i], n[i], dw[c][i]);
+                        sum = fmaf(g[i] * (kKeep ? w[kKeep ? c : 0][i] : again[i]), n[i], sum);
+                    }
+                }
+                const float mean = team_sum(sum, &scratch[turn][team * ring.team_warps], team, ring.team_warps) * inv;
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    const int col = 8 * (c * width + me);
+                    if (col >= cols) continue;
+                    float g[8], n[8], d[8] = {0, 0, 0, 0, 0, 0, 0, 0}, again[8];
+                    load8(p + col).unpack(g);
+                    load8(q + col).unpack(n);
+                    if (RES) load8(reinterpret_cast<const R*>(stage + ring.offset[2] + slot * ring.bytes[2]) + col).unpack(d);
+                    if (!kKeep) again_weight<T, W>(P, weights, col, again);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float gw = g[i] * (kKeep ? w[kKeep ? c : 0][i] : again[i]);
+                        g[i] = fmaf(r, fmaf(-(n[i] * r), mean, gw), d[i]);
+                    }
+                    store8(static_cast<R*>(a.dx) + row * a.lddx + col, g);
+                }
+            }
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&bars.empty[s]));
+        s += groups;
+        while (s >= ring.stages) s -= ring.stages, ++round;
+    }
+    if (a.dweight == nullptr) return;
+    // the teams' shares, added in their order through the ring's memory (every
+    // copy has landed and been read)
+    float* part = a.workspace + static_cast<int64_t>(blockIdx.x) * a.cols;
+    float* shares = reinterpret_cast<float*>(smem);
+    if (ring.teams > 1) {
+        const int all = ring.teams * width;
+        ptx::named_barrier_sync(15, all);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int col = 8 * (c * width + me);
+            if (col < cols) store8(shares + team * cols + col, dw[c]);
+        }
+        ptx::named_barrier_sync(15, all);
+        for (int col = threadIdx.x; col < cols; col += all) {
+            float v = shares[col];
+            for (int t = 1; t < ring.teams; ++t) v += shares[t * cols + col];
+            part[col] = v;
+        }
+    } else {
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int col = 8 * (c * width + me);
+            if (col < cols) store8(part + col, dw[c]);
+        }
+    }
+}
+
+// Rows too wide for registers: two passes over each row, and the CTA's share
+// of dweight is added up in its row of the workspace (every thread its own
+// columns).
+template <typename T, typename R>
+__global__ void __launch_bounds__(1024) rms_norm_grad_wide_kernel(const __grid_constant__ GradParams P) {
+    __shared__ float scratch[2][32];
+    ptx::let_next_grid_start();
+    ptx::wait_previous_grid();
+    const NormGradArgs& a = P.a;
+    const float inv = __frcp_rn(static_cast<float>(a.cols));
+    int turn = 0;
+    const bool same = a.weight_type == a.type;
+    auto weight = [&](int64_t j) {
+        return same ? to_f32(static_cast<const T*>(a.weight)[j]) : static_cast<const float*>(a.weight)[j];
+    };
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+        const T* dy = static_cast<const T*>(a.dy) + row * a.lddy;
+        const R* h = static_cast<const R*>(a.h) + row * a.ldh;
+        const float r = a.rstd[row];
+        float sum = 0.0f;
+        for (int64_t j = threadIdx.x; j < a.cols; j += blockDim.x)
+            sum = fmaf(to_f32(dy[j]) * weight(j), to_f32(h[j]) * r, sum);
+        const float mean = row_sum<false>(sum, scratch[turn]) * inv;
+        for (int64_t j = threadIdx.x; j < a.cols; j += blockDim.x) {
+            const float d = to_f32(dy[j]), n = to_f32(h[j]) * r;
+            const float more =
+                a.dresidual != nullptr ? to_f32(static_cast<const R*>(a.dresidual)[row * a.lddr + j]) : 0.0f;
+            static_cast<R*>(a.dx)[row * a.lddx + j] = from_f32<R>(fmaf(r, fmaf(-n, mean, d * weight(j)), more));
+            if (a.dweight != nullptr) {
+                float* part = a.workspace + static_cast<int64_t>(blockIdx.x) * a.cols + j;
+                *part = row == blockIdx.x ? d * n : fmaf(d, n, *part);
+            }
+        }
+    }
+}
+
+// dweight from the CTAs' shares: a CTA sums 32 columns, eight rows of
+// partials at a time, and adds the eight sums in order.
+__global__ void __launch_bounds__(256) sum_partials_kernel(const float* part, float* out, int64_t parts, int64_t cols) {
+    __shared__ float sums[8][32];
+    ptx::let_next_grid_start();
+    ptx::wait_previous_grid();
+    const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x % 32;
+    const int y = threadIdx.x / 32;
+    float v = 0.0f;
+    if (col < cols)
+        for (int64_t p = y; p < parts; p += 8) v += part[p * cols + col];
+    sums[y][threadIdx.x % 32] = v;
+    __syncthreads();
+    if (y == 0 && col < cols) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i) v += sums[i][threadIdx.x];
+        out[col] = v;
+    }
+}
+
+constexpr int64_t kGradSMs = 152;  // the partials' number is part of the interface (workspace size), so no device query
+
+template <typename T, typename R, int C>
+ap_status run_grad(const GradParams& P, int64_t grid, cudaStream_t stream) {
+    const int64_t chunks = (P.a.cols + 7) / 8;
+    const int threads = static_cast<int>(((chunks + C - 1) / C + 31) / 32 * 32);
+    record_launch(PATH_NORM_GRAD, grid, 8 * C, 0, 0, 0);
+    return launch_early(rms_norm_grad_kernel<T, R, C>, grid, threads, stream, P);
+}
+
+template <typename T, typename R, bool RES>
+ap_status launch_grad_ring(const DeviceInfo& di, const GradParams& P, const RowRing& ring, cudaStream_t stream) {
+    static std::atomic<int> configured[5][64];
+    if (ring.chunks == 2)
+        return launch_ring_kernel(di, rms_norm_grad_ring_kernel<T, R, 2, RES, IN_REGISTERS>, configured[0], P, ring, PATH_NORM_GRAD, stream);
+    if (ring.chunks == 3)
+        return ring.keep_weights
+                   ? launch_ring_kernel(di, rms_norm_grad_ring_kernel<T, R, 3, RES, IN_SHARED>, configured[1], P, ring, PATH_NORM_GRAD, stream)
+                   : launch_ring_kernel(di, rms_norm_grad_ring_kernel<T, R, 3, RES, IN_L2>, configured[2], P, ring, PATH_NORM_GRAD, stream);
+    return ring.keep_weights
+               ? launch_ring_kernel(di, rms_norm_grad_ring_kernel<T, R, 4, RES, IN_SHARED>, configured[3], P, ring, PATH_NORM_GRAD, stream)
+               : launch_ring_kernel(di, rms_norm_grad_ring_kernel<T, R, 4, RES, IN_L2>, configured[4], P, ring, PATH_NORM_GRAD, stream);
+}
+
+template <typename T, typename R>
+ap_status launch_grad_t(const DeviceInfo& di, const Options& o, const NormGradArgs& a, cudaStream_t stream) {
+    GradParams P;
+    P.a = a;
+    P.vec_dy = rows_aligned(a.dy, a.lddy, sizeof(T), 16);
+    P.vec_h = rows_aligned(a.h, a.ldh, sizeof(R), 16);
+    P.vec_r = rows_aligned(a.dresidual, a.lddr, sizeof(R), 16);
+    P.vec_dx = rows_aligned(a.dx, a.lddx, sizeof(R), 16);
+    P.vec_w = reinterpret_cast<uintptr_t>(a.weight) % 16 == 0;
+    int64_t grid = norm_grad_partials(a.rows, a.cols);
+    RowRing ring;
+    const void* const in[] = {a.dy, a.h, a.dresidual};
+    const int64_t ld[] = {a.lddy, a.ldh, a.lddr}, size[] = {sizeof(T), sizeof(R), sizeof(R)};
+    const bool res = a.dresidual != nullptr;
+    if (grid > 0) {
+        ap_status st;
+        if (P.vec_dx && P.vec_w && plan_ring(di, o, &ring, res ? 3 : 2, in, ld, size, a.rstd, a.rows, a.cols)) {
+            grid = ring_grid(ring, kGradSMs);
+            st = res ? launch_grad_ring<T, R, true>(di, P, ring, stream) : launch_grad_ring<T, R, false>(di, P, ring, stream);
+        } else {
+            if (a.cols <= 4096) {
+                st = run_grad<T, R, 1>(P, grid, stream);
+            } else if (a.cols <= 8192) {
+                st = run_grad<T, R, 2>(P, grid, stream);
+            } else if (a.cols <= 16384) {
+                st = run_grad<T, R, 4>(P, grid, stream);
+            } else {
+                record_launch(PATH_NORM_GRAD, grid, 0, 0, 0, 2);
+                st = launch_early(rms_norm_grad_wide_kernel<T, R>, grid, 1024, stream, P);
+            }
+        }
+        if (st != AP_OK) return st;
+    }
+    if (a.dweight == nullptr) return AP_OK;
+    return launch_early(sum_partials_kernel, (a.cols + 31) / 32, 256, stream, static_cast<const float*>(a.workspace),
+                        a.dweight, grid, a.cols);
+}
+
+}  // namespace
+
+// CTAs of the gradient's kernels at most: the ring runs one an SM, the others
+// two, each with at least one row.
+int64_t norm_grad_partials(int64_t rows, int64_t) { return std::min(rows, kGradSMs * 2); }
+
+ap_status launch_rms_norm_backward(const DeviceInfo& di, const Options& o, const NormGradArgs& a, cudaStream_t stream) {
+    const bool same = a.residual_type == a.type;
+    switch (a.type) {
+        case AP_BF16:
+            return same ? launch_grad_t<__nv_bfloat16, __nv_bfloat16>(di, o, a, stream)
+                        : launch_grad_t<__nv_bfloat16, float>(di, o, a, stream);
+        case AP_F16: return same ? launch_grad_t<__half, __half>(di, o, a, stream) : launch_grad_t<__half, float>(di, o, a, stream);
+        default: return launch_grad_t<float, float>(di, o, a, stream);
+    }
+}
+
+}  // namespace ap

@@ -528,3 +528,83 @@ def test_side_stream_and_graph(ap):
         g.replay()
         done(ap)
         assert torch.equal(state[-1], want)
+
+
+def test_quantize_scale_of_every_mantissa(ap):
+    """s = max(amax / 448, 2^-126) is the correctly rounded quotient for all 2^23 mantissas, at a middle exponent and where
+    the quotient becomes subnormal. (In 64 bits the quotient's second rounding is harmless: 53 >= 2 * 24 + 2 bits.)"""
+    for exponent in (0x3F800000, 0x04800000, 0x04000000):
+        x = (torch.arange(1 << 23, dtype=torch.int32, device="cuda") + exponent).view(torch.float32)[:, None]
+        q, s = torch.empty(1 << 23, 1, dtype=torch.uint8, device="cuda"), torch.empty(1 << 23, 1, device="cuda")
+        ap.ap_quantize(x, 1, q, s)
+        done(ap)
+        want = (x.double() / 448).float()
+        assert torch.equal(s, torch.where(want < fu.MIN_SCALE, torch.full_like(want, fu.MIN_SCALE), want))
+
+
+RING_SIZES = [(1, 8), (2, 200), (17, 512), (1500, 8), (999, 264), (400, 520), (700, 1000), (333, 2048), (311, 2056), (600, 5000),
+              (460, 8192), (307, 8200), (308, 16384)]
+
+
+@pytest.mark.parametrize("rows,cols", RING_SIZES)
+@pytest.mark.parametrize("kind,res", [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32"), ("f16", None)])
+def test_norm_ring_and_registers(ap, rows, cols, kind, res):
+    """Both forms of the norm on the same rows (1: the ring wherever it takes them, 2: the register form)."""
+    t = TYPES[kind]
+    x = randn(rows, cols, seed=cols).to(t)
+    residual = None if res is None else (2 * randn(rows, cols, seed=cols + 1)).to(TYPES[res])
+    weight = 1 + 0.1 * randn(cols, seed=2)
+    h, rr, yy = fu.norm(f64(x), None if res is None else f64(residual), f64(weight), 1e-5)
+    rel = (fu.DEPTH / 2 + 8) * U
+    for path in (1, 2):
+        ap.ap_debug_set(ap.AP_DBG_FORCE_PATH, path)
+        out = None if res is None else torch.full_like(residual, float("nan"))
+        y, q = torch.full_like(x, float("nan")), empty8(rows, cols)
+        s, r = torch.empty(rows, fu.blocks(cols), device="cuda"), torch.empty(rows, device="cuda")
+        ap.ap_rms_norm(x, weight, 1e-5, y=y, q=q, q_scales=s, residual=residual, residual_out=out, rstd=r)
+        done(ap)
+        # (past 8192 columns two stages of a row of both types may not fit)
+        assert ap.ap_debug_get(ap.AP_DBG_LAST_FLAGS) == 4 or path == 2 or cols > 8192
+        assert np.all(np.abs(f64(r) - rr) <= rel * rr)
+        assert np.all(np.abs(f64(y) - yy) <= fu.rounding(yy, t) * (1 + rel) + rel * np.abs(yy))
+        if res is not None:
+            assert np.all(np.abs(f64(out) - h) <= fu.rounding(h, out.dtype) * (1 + U) + U * np.abs(h))
+        fu.check_codes(q, s, yy, 1, rel, f"norm {rows}x{cols} path {path}")
+
+
+@pytest.mark.parametrize("shift,pad", [(0, 8), (8, 24)])
+def test_norm_ring_strided_rows_stay_inside(ap, shift, pad):
+    rows, cols, t = 700, 1032, torch.bfloat16
+    ap.ap_debug_set(ap.AP_DBG_FORCE_PATH, 1)
+    x = Strided(rows, cols, t, cols + pad, shift, randn(rows, cols).to(t))
+    res = Strided(rows, cols, torch.float32, cols + 2 * pad, shift, randn(rows, cols, seed=1))
+    q = Strided(rows, cols, torch.uint8, cols + pad, shift)
+    s, w = torch.empty(rows, fu.blocks(cols), device="cuda"), randn(cols, seed=2)
+    h, rr, yy = fu.norm(f64(x.view), f64(res.view), f64(w), 0.0)
+    ap.ap_rms_norm(x.view, w, 0.0, y=x.view, q=q.view, q_scales=s, residual=res.view, residual_out=res.view)
+    done(ap)
+    assert ap.ap_debug_get(ap.AP_DBG_LAST_FLAGS) == 4 and all(b.intact() for b in (x, res, q))
+    rel = (fu.DEPTH / 2 + 8) * U
+    assert np.all(np.abs(f64(x.view) - yy) <= fu.rounding(yy, t) * (1 + rel) + rel * np.abs(yy))
+    assert np.all(np.abs(f64(res.view) - h) <= fu.rounding(h, torch.float32) + U * np.abs(h))
+    fu.check_codes(q.view.clone().view(E4M3), s, yy, 1, rel, "strided ring norm")
+
+
+def test_norm_ring_bounded_wait(ap):
+    """Rows that never arrive: both ring kernels give up, the error is reported once, and the next calls work."""
+    x, w = randn(2000, 512), torch.ones(512, device="cuda")
+    y, r = torch.empty_like(x), torch.empty(2000, device="cuda")
+    ap.ap_debug_set(ap.AP_DBG_FORCE_PATH, 1)
+    ap.ap_rms_norm(x, w, 1e-6, y=y, rstd=r)
+    done(ap)
+    want, dx = y.clone(), torch.empty_like(x)
+    for call in (lambda: ap.ap_rms_norm(x, w, 1e-6, y=y), lambda: ap.ap_rms_norm_backward(x, x, w, r, dx)):
+        ap.ap_debug_set(ap.AP_DBG_TIMEOUT_NS, 2_000_000)
+        ap.ap_debug_set(ap.AP_DBG_EXPECT_TX_EXTRA, 16)
+        call()
+        assert ap.ap_check() == ap.AP_ERR_DEVICE_TIMEOUT
+        reset_debug(ap)
+        ap.ap_debug_set(ap.AP_DBG_FORCE_PATH, 1)
+        call()
+        done(ap)
+    assert torch.equal(y, want)
