@@ -6,6 +6,7 @@
 #include <cuda_fp16.h>
 
 #include <cstdint>
+#include <type_traits>
 
 namespace ap {
 
@@ -167,6 +168,49 @@ __device__ __forceinline__ float amax3(float a, float b, float c) {
 __device__ __forceinline__ float amax8(const float (&v)[8]) {
     return amax3(amax3(v[0], v[1], v[2]), amax3(v[3], v[4], v[5]), amax3(v[6], v[7], 0.0f));
 }
+
+// Largest magnitudes of 16-bit values two at a time in their own type (exact:
+// a maximum rounds nothing), of floats one at a time; NaN where a value is.
+template <typename T>
+struct Peak {  // 16-bit types: V holds two running maxima
+    using V = uint32_t;
+    static constexpr int kWords = 4;  // V's of a chunk of eight, for maxima by column
+    static __device__ __forceinline__ V max(V a, V b) {
+        V r;
+        if constexpr (std::is_same_v<T, __half>)
+            asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        else
+            asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
+    static __device__ __forceinline__ V word(const Raw8<T>& r, int i) {
+        return (i == 0 ? r.w.x : (i == 1 ? r.w.y : (i == 2 ? r.w.z : r.w.w))) & 0x7FFF7FFFu;
+    }
+    static __device__ __forceinline__ V chunk(const Raw8<T>& r) { return max(max(word(r, 0), word(r, 1)), max(word(r, 2), word(r, 3))); }
+    static __device__ __forceinline__ float value(V v) {
+        const float2 f = unpack2(v, T());
+        return max_nan(f.x, f.y);
+    }
+    static __device__ __forceinline__ float column(const V (&v)[kWords], int i) {
+        const float2 f = unpack2(v[i / 2], T());
+        return i % 2 ? f.y : f.x;
+    }
+};
+template <>
+struct Peak<float> {
+    using V = float;
+    static constexpr int kWords = 8;
+    static __device__ __forceinline__ V max(V a, V b) { return max_nan(a, b); }
+    static __device__ __forceinline__ V word(const Raw8<float>& r, int i) {
+        const float v[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+        return fabsf(v[i]);
+    }
+    static __device__ __forceinline__ V chunk(const Raw8<float>& r) {
+        return amax3(amax3(r.a.x, r.a.y, r.a.z), amax3(r.a.w, r.b.x, r.b.y), amax3(r.b.z, r.b.w, 0.0f));
+    }
+    static __device__ __forceinline__ float value(V v) { return v; }
+    static __device__ __forceinline__ float column(const V (&v)[kWords], int i) { return v[i]; }
+};
 
 // A block's scale s = max(amax / 448, 2^-126) and 1 / s, both rounded to
 // nearest. Every half warp of the norm and the quantiser computes them once a
