@@ -60,18 +60,18 @@ struct MatmulParams {
 
 template <int BN, int CG, int STAGES, bool PER_COL, bool SWAP>
 struct Form {
-    static constexpr int kGroups = BN >= 128 ? 2 : 1;    // consumer groups, side by side along the columns
+    static constexpr int kGroups = BN < 128 ? 1 : 2;  // consumer groups, side by side along the columns
     static constexpr int kCols = BN / kGroups;           // columns of a group
     static constexpr int kMmaGroups = BN > 128 ? 2 : 1;  // matrix instructions side by side
     static constexpr int kMmaCols = BN / kMmaGroups;     // columns of one
     static constexpr int kConsumerWarps = 4 * kGroups;
     static constexpr int kThreads = 32 * (kConsumerWarps + 4);
-    // The widest form: 384 threads of 168 registers at launch (64512), shared out
-    // anew: 128 sums and the loads under way need more than 168. With scales
-    // by column, 16 columns a load are what fits without spills.
+    // The widest form: 384 threads of 168 registers at launch (64512), shared
+    // out anew: 128 sums and the loads under way need more than 168. With
+    // scales by column, 16 columns a load are what fits without spills.
     static constexpr int kOtherRegs = PER_COL ? 56 : 72, kConsumerRegs = PER_COL ? 224 : 216;
-    static_assert(128 * kOtherRegs + 256 * kConsumerRegs <= 384 * 168, "registers of the launch");
-    static constexpr int kLoad = BN <= 64 || PER_COL ? 16 : 32;
+    static constexpr int kLoad = 16;
+    static_assert(BN <= 128 || 128 * kOtherRegs + 256 * kConsumerRegs <= 384 * 168, "registers of the launch");
     static constexpr int kQBox = kMmaCols / CG;  // rows of Q this CTA loads for one instruction
     static constexpr uint32_t kPBytes = kTile * kTile, kQBytes = kQBox * kTile;
     static constexpr uint32_t kStageBytes = kPBytes + kMmaGroups * kQBytes;
@@ -83,8 +83,9 @@ struct Form {
     static constexpr uint32_t kTmemCols = kBuffers * kRun * BN;
     // CTAs an SM: the narrow forms wait more than they compute
     static constexpr int kCtas = BN > 64 ? 1 : 2;
-    // c leaves through shared memory: 4 KiB a consumer warp, 32 rows of 128 bytes
-    static constexpr uint32_t kStagingBytes = SWAP ? 0 : 4096 * kConsumerWarps;
+    // c leaves through shared memory: a consumer warp's 32 rows of 64 or 128 bytes
+    static constexpr uint32_t kStagingRow = 128;
+    static constexpr uint32_t kStagingBytes = SWAP ? 0 : 32 * kStagingRow * kConsumerWarps;
     static constexpr size_t kRingBytes = size_t(STAGES) * kStageBytes;
     static constexpr size_t kSmem = kRingBytes + kStagingBytes + 1024;
     // a split tile's shares: rows of BN floats, padded so that the 32 rows a
@@ -191,13 +192,14 @@ __global__ void __launch_bounds__(Form<BN, CG, STAGES, PER_COL, SWAP>::kThreads,
 
     // A wait that gives up ends its role; the CTA's abort flag ends the
     // others. The first probes go without wait_phase's clock reads.
-    auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
+    auto wait_at = [&](uint32_t bar, uint32_t parity, uint32_t site) {
         for (int i = 0; i < 64; ++i)
-            if (ptx::mbar_try_wait(ptx::smem_addr(bar), parity)) return true;
-        const int w = wait_phase<false>(ptx::smem_addr(bar), parity, P.timeout_ns, abort_flag);
+            if (ptx::mbar_try_wait(bar, parity)) return true;
+        const int w = wait_phase<false>(bar, parity, P.timeout_ns, abort_flag);
         if (w == WAIT_TIMEOUT) raise_timeout(P.status, site, abort_flag);
         return w == WAIT_OK;
     };
+    auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) { return wait_at(ptx::smem_addr(bar), parity, site); };
 
     // For a whole warp: one lane asks, since 32 lanes' probes of a barrier are
     // served one after another and hold up every other barrier of the SM.
@@ -334,8 +336,20 @@ __global__ void __launch_bounds__(Form<BN, CG, STAGES, PER_COL, SWAP>::kThreads,
         const int group = warp / 4, quad = warp % 4;
         const int source = group * F::kMmaGroups / F::kGroups;  // the matrix instructions whose columns these are
         const int my_row = 32 * quad + lane;  // accumulator row of this thread, in the CTA's 128
-        const uint32_t staging = ring + static_cast<uint32_t>(F::kRingBytes) + 4096u * warp;
-        uint32_t step = 0, run = 0;
+        const uint32_t staging = ring + static_cast<uint32_t>(F::kRingBytes) + 32 * F::kStagingRow * warp;
+        // Where the walk over blocks stands, kept as offsets and parities that
+        // step with it: the index arithmetic of a block would otherwise be a
+        // quarter of its instructions.
+        static_assert(F::kBuffers == 2 && kScaleSlots == 2, "two of each in turn");
+        constexpr uint32_t kBarStep = 8 * F::kMmaGroups;  // from a buffer's barrier to the other's
+        const uint32_t full_bars = ptx::smem_addr(&sh.acc_full[0][source]), empty_bars = ptx::smem_addr(&sh.acc_empty[0][source]);
+        const uint32_t free_bars = CG == 2 ? ptx::mapa(empty_bars, 0) : empty_bars;
+        const uint32_t lanes = tmem + group * kCols + (static_cast<uint32_t>(32 * quad) << 16);
+        const float* const row_scale = &sh.row_scales[0][0][my_row];
+        const float* const col_scale = &sh.col_scales[0][0][PER_COL ? group * kCols : group];
+        constexpr int kRowPitch = sizeof(sh.row_scales[0][0]) / 4, kColPitch = sizeof(sh.col_scales[0][0]) / 4;
+        uint32_t buf = 0, phase = 0;   // accumulator, and its barrier's parity
+        uint32_t spot = 0, scale_phase = 0;  // block's scales, kScaleRun a slot, and the slots' parity
         bool ok = true;
         for (int32_t t = first_tile; t < tiles; t += tile_step) {
             int32_t tp, tq;
@@ -345,82 +359,71 @@ __global__ void __launch_bounds__(Form<BN, CG, STAGES, PER_COL, SWAP>::kThreads,
             for (int j = 0; j < kCols; ++j) acc[j] = 0.0f;
             // A warp takes the blocks one after another, so what it waits for
             // is taken off that path: the next accumulator's barrier is asked
-            // before this one's last sums, the next load from tensor memory
-            // (the next block's first one included) is under way while the
-            // sums of the current one are taken, and nothing on the path
-            // branches by lane.
-            float v[2][kLoad];
-            const uint32_t lanes = tmem + group * kCols + (static_cast<uint32_t>(32 * quad) << 16);
-            ok = ok && warp_wait(&sh.acc_full[step % F::kBuffers][source], (step / F::kBuffers) & 1, SITE_MM_CONSUMER_ACC);
-            ok = ok && warp_wait(&sh.scales_full[run % kScaleSlots], (run / kScaleSlots) & 1, SITE_MM_SCALES_FULL);
-            if (ok) {
-                ptx::tcgen05_fence_after();
-                ptx::tmem_ld(lanes + (step % F::kBuffers) * F::kRun * BN, v[0]);
-            }
+            // before this one's sums, a load from tensor memory is under way
+            // while the sums of the one before are taken, and nothing on the
+            // path branches by lane. (A load carried over to the next block
+            // costs a move a register; starting each block afresh is faster.)
+            ok = ok && warp_wait(&sh.scales_full[spot / kScaleRun], scale_phase, SITE_MM_SCALES_FULL);
+            ok = ok && warp_wait(&sh.acc_full[buf][source], phase, SITE_MM_CONSUMER_ACC);
             int j = 0;  // block of the accumulator
-            for (int32_t kb = kb0; kb < kb1 && ok; ++kb) {
-                const uint32_t buf = step % F::kBuffers, slot = run % kScaleSlots;
-                const uint32_t next = step + 1, next_buf = next % F::kBuffers;
-                const int e = (kb - kb0) % kScaleRun;
-                const bool last = kb + 1 == kb1;
-                const bool over = F::kRun == 1 || j == F::kRun - 1 || last;  // the accumulator's last block
+            for (int32_t left = kb1 - kb0; left > 0 && ok; --left) {
+                const bool over = F::kRun == 1 || j == F::kRun - 1 || left == 1;  // the accumulator's last block
+                const uint32_t at = lanes + (buf * F::kRun + j) * BN;
+                const uint32_t next_phase = phase ^ buf;  // the other buffer's parity when its turn comes
+                float v[2][kLoad];
+                ptx::tcgen05_fence_after();
+                ptx::tmem_ld(at, v[0]);
                 bool ready = false;
                 if (over)  // (after the last block the answer is not used)
-                    ready = ptx::mbar_test(ptx::smem_addr(&sh.acc_full[next_buf][source]), (next / F::kBuffers) & 1);
-                float scale = sh.row_scales[slot][e][my_row];
-                if (!PER_COL) scale *= sh.col_scales[slot][e][group];
-                const uint32_t at = lanes + (buf * F::kRun + j) * BN;
-                const uint32_t after = over ? lanes + next_buf * F::kRun * BN : at + BN;  // the next block's columns
+                    ready = ptx::mbar_test(full_bars + (buf ^ 1) * kBarStep, next_phase);
+                float scale = row_scale[spot * kRowPitch];
+                const float* const cols_at = col_scale + spot * kColPitch;
+                if (!PER_COL) scale *= *cols_at;
 #pragma unroll
                 for (int g = 0; g < kLoads; ++g) {
-                    ptx::tmem_wait_ld(v[g % 2]);
+                    ptx::tmem_wait_ld();
                     if (g + 1 < kLoads) {
                         ptx::tmem_ld(at + kLoad * (g + 1), v[(g + 1) % 2]);
-                    } else {
-                        if (over) {
-                            // all of the accumulator is in registers: it is
-                            // free before the last sums are taken
-                            ptx::tcgen05_fence_before();
-                            __syncwarp();
-                            const uint32_t bar = ptx::smem_addr(&sh.acc_empty[buf][source]);
-                            ptx::mbar_arrive_if<CG == 2>(lane == 0, CG == 2 ? ptx::mapa(bar, 0) : bar);
-                            if (!last) {
-                                if (!ready)
-                                    ready = wait(&sh.acc_full[next_buf][source], (next / F::kBuffers) & 1, SITE_MM_CONSUMER_ACC);
-                                ok = __all_sync(0xffffffffu, ready);
-                                ptx::tcgen05_fence_after();
-                                if (ok && kLoads % 2 == 0) ptx::tmem_ld(after, v[0]);
-                            }
-                        } else if (kLoads % 2 == 0) {
-                            ptx::tmem_ld(after, v[0]);
-                        }
+                    } else if (over) {
+                        // all of the accumulator is in registers: it is free
+                        // before the last sums are taken
+                        ptx::tcgen05_fence_before();
+                        __syncwarp();
+                        ptx::mbar_arrive_if<CG == 2>(lane == 0, free_bars + buf * kBarStep);
                     }
 #pragma unroll
                     for (int i = 0; i < kLoad; i += 4) {
                         const int col = kLoad * g + i;
                         float4 cs = make_float4(scale, scale, scale, scale);
                         if (PER_COL) {
-                            cs = *reinterpret_cast<const float4*>(&sh.col_scales[slot][e][PER_COL ? group * kCols + col : 0]);
+                            cs = *reinterpret_cast<const float4*>(cols_at + col);
                             cs.x *= scale, cs.y *= scale, cs.z *= scale, cs.w *= scale;
                         }
-                        acc[col] = fmaf(v[g % 2][i], cs.x, acc[col]);
-                        acc[col + 1] = fmaf(v[g % 2][i + 1], cs.y, acc[col + 1]);
-                        acc[col + 2] = fmaf(v[g % 2][i + 2], cs.z, acc[col + 2]);
-                        acc[col + 3] = fmaf(v[g % 2][i + 3], cs.w, acc[col + 3]);
+                        acc[col] = ptx::fma_ordered(v[g % 2][i], cs.x, acc[col]);
+                        acc[col + 1] = ptx::fma_ordered(v[g % 2][i + 1], cs.y, acc[col + 1]);
+                        acc[col + 2] = ptx::fma_ordered(v[g % 2][i + 2], cs.z, acc[col + 2]);
+                        acc[col + 3] = ptx::fma_ordered(v[g % 2][i + 3], cs.w, acc[col + 3]);
                     }
                 }
-                // one load a block: its registers are free only now
-                if (kLoads % 2 != 0 && ok && !last) ptx::tmem_ld(after, v[0]);
+                if (over) {
+                    if (left > 1) {
+                        if (!ready) ready = wait_at(full_bars + (buf ^ 1) * kBarStep, next_phase, SITE_MM_CONSUMER_ACC);
+                        ok = __all_sync(0xffffffffu, ready);
+                    }
+                    phase = next_phase;
+                    buf ^= 1;
+                }
                 if (F::kRun > 1) j = over ? 0 : j + 1;
-                step += over ? 1 : 0;
-                if (e == kScaleRun - 1 || last) {  // this run's scales have been read
+                ++spot;
+                if (spot % kScaleRun == 0 || left == 1) {  // this run's scales have been read
+                    const uint32_t slot = (spot - 1) / kScaleRun;
                     __syncwarp();
                     ptx::mbar_arrive_if<false>(lane == 0, ptx::smem_addr(&sh.scales_empty[slot]));
-                    ++run;
-                    if (!last && ok) {
-                        uint64_t* bar = &sh.scales_full[run % kScaleSlots];
-                        ok = __all_sync(0xffffffffu, wait(bar, (run / kScaleSlots) & 1, SITE_MM_SCALES_FULL));
-                    }
+                    spot = (slot ^ 1) * kScaleRun;
+                    scale_phase ^= slot;
+                    if (left > 1 && ok)
+                        ok = __all_sync(0xffffffffu, wait_at(ptx::smem_addr(&sh.scales_full[slot ^ 1]), scale_phase,
+                                                             SITE_MM_SCALES_FULL));
                 }
             }
             const int64_t row = (static_cast<int64_t>(tp) * CG + (CG == 2 ? rank : 0)) * kTile + my_row;
@@ -440,17 +443,17 @@ __global__ void __launch_bounds__(Form<BN, CG, STAGES, PER_COL, SWAP>::kThreads,
                     }
                 }
             } else if (!SWAP && F::kStagingBytes > 0 && P.vec_c) {
-                // 32 rows x 128 bytes at a time through the warp's staging:
+                // 32 rows x 64 or 128 bytes at a time through the warp's staging:
                 // 16-byte units at the places the tensor map's swizzle gives
                 // them, so a warp's writes meet no bank twice
-                constexpr int kPiece = 128 / sizeof(C), kUnit = 16 / sizeof(C);
+                constexpr int kPiece = F::kStagingRow / sizeof(C), kUnit = 16 / sizeof(C);
                 if (ok) {
 #pragma unroll
                     for (int piece = 0; piece < (F::kStagingBytes > 0 ? kCols / kPiece : 0); ++piece) {
                         if (lane == 0) ptx::bulk_wait_read<0>();  // the previous piece has left
                         __syncwarp();
 #pragma unroll
-                        for (int u = 0; u < 8; ++u) {
+                        for (int u = 0; u < static_cast<int>(F::kStagingRow / 16); ++u) {
                             const int j = piece * kPiece + u * kUnit;
                             uint4 w;
                             if constexpr (sizeof(C) == 4)
@@ -458,7 +461,7 @@ __global__ void __launch_bounds__(Form<BN, CG, STAGES, PER_COL, SWAP>::kThreads,
                             else
                                 w = make_uint4(pack2<C>(acc[j], acc[j + 1]), pack2<C>(acc[j + 2], acc[j + 3]),
                                                pack2<C>(acc[j + 4], acc[j + 5]), pack2<C>(acc[j + 6], acc[j + 7]));
-                            st_shared4(staging + 128 * lane + 16 * (u ^ (lane & 7)), w);
+                            st_shared4(staging + F::kStagingRow * lane + 16 * (u ^ (F::kStagingRow == 128 ? lane & 7 : (lane >> 1) & 3)), w);
                         }
                         ptx::fence_proxy_async_smem();
                         __syncwarp();
@@ -543,17 +546,18 @@ __global__ void __launch_bounds__(Form<BN, CG, STAGES, PER_COL, SWAP>::kThreads,
     }
 }
 
-// A matrix of rows x cols elements as boxes of 128 bytes by box_rows rows.
+// A matrix of rows x cols elements as boxes of 64 or 128 bytes by box_rows
+// rows, in the swizzle of that width.
 bool box_map(CUtensorMap* map, CUtensorMapDataType type, const void* p, int64_t size, int64_t rows, int64_t cols, int64_t ld,
-             uint32_t box_rows) {
+             uint32_t box_rows, uint32_t box_bytes = 128) {
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld * size)};
-    const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / size), box_rows};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_bytes / size), box_rows};
     const cuuint32_t estr[2] = {1, 1};
     auto encode = tensor_map_encoder();
     return encode != nullptr &&
            encode(map, type, 2, const_cast<void*>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                  box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Launch configuration of a form's grid in clusters.
@@ -636,7 +640,7 @@ ap_status launch_form(const DeviceInfo& di, MatmulParams P, const MatmulArgs& a,
         return AP_ERR_CUDA;
     if (!SWAP && P.split == 1 && P.vec_c &&
         !box_map(&mc, sizeof(C) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, a.c, sizeof(C), a.m,
-                 a.n, a.ldc, 32))
+                 a.n, a.ldc, 32, F::kStagingRow))
         return AP_ERR_CUDA;
     const int cluster = CG == 2 ? 2 : P.split;
     int64_t grid = tiles * cluster;
