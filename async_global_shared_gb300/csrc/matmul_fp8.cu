@@ -78,8 +78,8 @@ struct Form {
     // Accumulators: the products of kRun blocks of k side by side are handed
     // over at once (a hand-over costs hundreds of cycles whatever its size),
     // in two buffers. The widest form fills tensor memory with one block each.
-    static constexpr int kRun = BN > 128 ? 1 : (BN > 32 ? 2 : 4);
-    static constexpr int kBuffers = 2;
+    static constexpr int kRun = CG == 2 ? 1 : 2;
+    static constexpr int kBuffers = CG == 2 ? 512 / BN : 2;
     static constexpr uint32_t kTmemCols = kBuffers * kRun * BN;
     // CTAs an SM: the narrow forms wait more than they compute
     static constexpr int kCtas = BN > 64 ? 1 : 2;
@@ -340,8 +340,8 @@ __global__ void __launch_bounds__(Form<BN, CG, STAGES, PER_COL, SWAP>::kThreads,
         // Where the walk over blocks stands, kept as offsets and parities that
         // step with it: the index arithmetic of a block would otherwise be a
         // quarter of its instructions.
-        static_assert(F::kBuffers == 2 && kScaleSlots == 2, "two of each in turn");
-        constexpr uint32_t kBarStep = 8 * F::kMmaGroups;  // from a buffer's barrier to the other's
+        static_assert(kScaleSlots == 2, "two in turn");
+        constexpr uint32_t kBarStep = 8 * F::kMmaGroups;  // from a buffer's barrier to the next
         const uint32_t full_bars = ptx::smem_addr(&sh.acc_full[0][source]), empty_bars = ptx::smem_addr(&sh.acc_empty[0][source]);
         const uint32_t free_bars = CG == 2 ? ptx::mapa(empty_bars, 0) : empty_bars;
         const uint32_t lanes = tmem + group * kCols + (static_cast<uint32_t>(32 * quad) << 16);
@@ -369,13 +369,13 @@ __global__ void __launch_bounds__(Form<BN, CG, STAGES, PER_COL, SWAP>::kThreads,
             for (int32_t left = kb1 - kb0; left > 0 && ok; --left) {
                 const bool over = F::kRun == 1 || j == F::kRun - 1 || left == 1;  // the accumulator's last block
                 const uint32_t at = lanes + (buf * F::kRun + j) * BN;
-                const uint32_t next_phase = phase ^ buf;  // the other buffer's parity when its turn comes
+                const uint32_t next_buf = (buf + 1) % F::kBuffers, next_phase = phase ^ (next_buf == 0 ? 1u : 0u);
                 float v[2][kLoad];
                 ptx::tcgen05_fence_after();
                 ptx::tmem_ld(at, v[0]);
                 bool ready = false;
                 if (over)  // (after the last block the answer is not used)
-                    ready = ptx::mbar_test(full_bars + (buf ^ 1) * kBarStep, next_phase);
+                    ready = ptx::mbar_test(full_bars + next_buf * kBarStep, next_phase);
                 float scale = row_scale[spot * kRowPitch];
                 const float* const cols_at = col_scale + spot * kColPitch;
                 if (!PER_COL) scale *= *cols_at;
@@ -407,11 +407,11 @@ __global__ void __launch_bounds__(Form<BN, CG, STAGES, PER_COL, SWAP>::kThreads,
                 }
                 if (over) {
                     if (left > 1) {
-                        if (!ready) ready = wait_at(full_bars + (buf ^ 1) * kBarStep, next_phase, SITE_MM_CONSUMER_ACC);
+                        if (!ready) ready = wait_at(full_bars + next_buf * kBarStep, next_phase, SITE_MM_CONSUMER_ACC);
                         ok = __all_sync(0xffffffffu, ready);
                     }
                     phase = next_phase;
-                    buf ^= 1;
+                    buf = next_buf;
                 }
                 if (F::kRun > 1) j = over ? 0 : j + 1;
                 ++spot;
