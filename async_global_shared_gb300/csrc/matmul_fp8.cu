@@ -67,10 +67,8 @@ struct Form {
     static constexpr int kConsumerWarps = 4 * kGroups;
     static constexpr int kThreads = 32 * (kConsumerWarps + 4);
     // The widest form: 384 threads of 168 registers at launch (64512), shared
-    // out anew: 128 sums and the loads under way need more than 168. With
-    // scales by column, 16 columns a load are what fits without spills.
+    // out anew: 128 sums and the loads under way need more than 168.
     static constexpr int kOtherRegs = PER_COL ? 56 : 72, kConsumerRegs = PER_COL ? 224 : 216;
-    static constexpr int kLoad = 16;
     static_assert(BN <= 128 || 128 * kOtherRegs + 256 * kConsumerRegs <= 384 * 168, "registers of the launch");
     static constexpr int kQBox = kMmaCols / CG;  // rows of Q this CTA loads for one instruction
     static constexpr uint32_t kPBytes = kTile * kTile, kQBytes = kQBox * kTile;
@@ -83,9 +81,8 @@ struct Form {
     static constexpr uint32_t kTmemCols = kBuffers * kRun * BN;
     // CTAs an SM: the narrow forms wait more than they compute
     static constexpr int kCtas = BN > 64 ? 1 : 2;
-    // c leaves through shared memory: a consumer warp's 32 rows of 64 or 128 bytes
-    static constexpr uint32_t kStagingRow = 128;
-    static constexpr uint32_t kStagingBytes = SWAP ? 0 : 32 * kStagingRow * kConsumerWarps;
+    // c leaves through shared memory: a consumer warp's 32 rows of 128 bytes
+    static constexpr uint32_t kStagingBytes = SWAP ? 0 : 32 * 128 * kConsumerWarps;
     static constexpr size_t kRingBytes = size_t(STAGES) * kStageBytes;
     static constexpr size_t kSmem = kRingBytes + kStagingBytes + 1024;
     // a split tile's shares: rows of BN floats, padded so that the 32 rows a
@@ -331,12 +328,12 @@ __global__ void __launch_bounds__(Form<BN, CG, STAGES, PER_COL, SWAP>::kThreads,
         }
     } else {  // consumers
         if (BN > 128) ptx::regs_more<F::kConsumerRegs>();
-        constexpr int kLoad = F::kLoad;  // columns of one load from tensor memory
+        constexpr int kLoad = 16;  // columns of one load from tensor memory
         constexpr int kLoads = kCols / kLoad;
         const int group = warp / 4, quad = warp % 4;
         const int source = group * F::kMmaGroups / F::kGroups;  // the matrix instructions whose columns these are
         const int my_row = 32 * quad + lane;  // accumulator row of this thread, in the CTA's 128
-        const uint32_t staging = ring + static_cast<uint32_t>(F::kRingBytes) + 32 * F::kStagingRow * warp;
+        const uint32_t staging = ring + static_cast<uint32_t>(F::kRingBytes) + 32 * 128 * warp;
         // Where the walk over blocks stands, kept as offsets and parities that
         // step with it: the index arithmetic of a block would otherwise be a
         // quarter of its instructions.
@@ -374,8 +371,6 @@ __global__ void __launch_bounds__(Form<BN, CG, STAGES, PER_COL, SWAP>::kThreads,
                 ptx::tcgen05_fence_after();
                 ptx::tmem_ld(at, v[0]);
                 bool ready = false;
-                if (over)  // (after the last block the answer is not used)
-                    ready = ptx::mbar_test(full_bars + next_buf * kBarStep, next_phase);
                 float scale = row_scale[spot * kRowPitch];
                 const float* const cols_at = col_scale + spot * kColPitch;
                 if (!PER_COL) scale *= *cols_at;
@@ -390,6 +385,7 @@ __global__ void __launch_bounds__(Form<BN, CG, STAGES, PER_COL, SWAP>::kThreads,
                         ptx::tcgen05_fence_before();
                         __syncwarp();
                         ptx::mbar_arrive_if<CG == 2>(lane == 0, free_bars + buf * kBarStep);
+                        ready = ptx::mbar_test(full_bars + next_buf * kBarStep, next_phase);
                     }
 #pragma unroll
                     for (int i = 0; i < kLoad; i += 4) {
@@ -442,18 +438,18 @@ __global__ void __launch_bounds__(Form<BN, CG, STAGES, PER_COL, SWAP>::kThreads,
                         st_shared4(ring + 4 * (my_row * F::kSharePitch + col), as_words(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]));
                     }
                 }
-            } else if (!SWAP && F::kStagingBytes > 0 && P.vec_c) {
-                // 32 rows x 64 or 128 bytes at a time through the warp's staging:
+            } else if (!SWAP && P.vec_c) {
+                // 32 rows x 128 bytes at a time through the warp's staging:
                 // 16-byte units at the places the tensor map's swizzle gives
                 // them, so a warp's writes meet no bank twice
-                constexpr int kPiece = F::kStagingRow / sizeof(C), kUnit = 16 / sizeof(C);
+                constexpr int kPiece = 128 / sizeof(C), kUnit = 16 / sizeof(C);
                 if (ok) {
 #pragma unroll
-                    for (int piece = 0; piece < (F::kStagingBytes > 0 ? kCols / kPiece : 0); ++piece) {
+                    for (int piece = 0; piece < (SWAP ? 0 : kCols / kPiece); ++piece) {
                         if (lane == 0) ptx::bulk_wait_read<0>();  // the previous piece has left
                         __syncwarp();
 #pragma unroll
-                        for (int u = 0; u < static_cast<int>(F::kStagingRow / 16); ++u) {
+                        for (int u = 0; u < 8; ++u) {
                             const int j = piece * kPiece + u * kUnit;
                             uint4 w;
                             if constexpr (sizeof(C) == 4)
@@ -461,7 +457,7 @@ __global__ void __launch_bounds__(Form<BN, CG, STAGES, PER_COL, SWAP>::kThreads,
                             else
                                 w = make_uint4(pack2<C>(acc[j], acc[j + 1]), pack2<C>(acc[j + 2], acc[j + 3]),
                                                pack2<C>(acc[j + 4], acc[j + 5]), pack2<C>(acc[j + 6], acc[j + 7]));
-                            st_shared4(staging + F::kStagingRow * lane + 16 * (u ^ (F::kStagingRow == 128 ? lane & 7 : (lane >> 1) & 3)), w);
+                            st_shared4(staging + 128 * lane + 16 * (u ^ (lane & 7)), w);
                         }
                         ptx::fence_proxy_async_smem();
                         __syncwarp();
@@ -490,7 +486,7 @@ __global__ void __launch_bounds__(Form<BN, CG, STAGES, PER_COL, SWAP>::kThreads,
                 }
             }
         }
-        if (!SWAP && F::kStagingBytes > 0 && lane == 0) ptx::bulk_wait_all();
+        if (!SWAP && lane == 0) ptx::bulk_wait_all();
     }
     __syncwarp();  // the one-thread roles' idle lanes wait here
     ptx::tcgen05_fence_before();
@@ -546,18 +542,18 @@ __global__ void __launch_bounds__(Form<BN, CG, STAGES, PER_COL, SWAP>::kThreads,
     }
 }
 
-// A matrix of rows x cols elements as boxes of 64 or 128 bytes by box_rows
-// rows, in the swizzle of that width.
+// A matrix of rows x cols elements as boxes of 128 bytes by box_rows rows, in
+// the swizzle of that width.
 bool box_map(CUtensorMap* map, CUtensorMapDataType type, const void* p, int64_t size, int64_t rows, int64_t cols, int64_t ld,
-             uint32_t box_rows, uint32_t box_bytes = 128) {
+             uint32_t box_rows) {
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld * size)};
-    const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_bytes / size), box_rows};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / size), box_rows};
     const cuuint32_t estr[2] = {1, 1};
     auto encode = tensor_map_encoder();
     return encode != nullptr &&
            encode(map, type, 2, const_cast<void*>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Launch configuration of a form's grid in clusters.
@@ -640,7 +636,7 @@ ap_status launch_form(const DeviceInfo& di, MatmulParams P, const MatmulArgs& a,
         return AP_ERR_CUDA;
     if (!SWAP && P.split == 1 && P.vec_c &&
         !box_map(&mc, sizeof(C) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, a.c, sizeof(C), a.m,
-                 a.n, a.ldc, 32, F::kStagingRow))
+                 a.n, a.ldc, 32))
         return AP_ERR_CUDA;
     const int cluster = CG == 2 ? 2 : P.split;
     int64_t grid = tiles * cluster;
@@ -669,11 +665,13 @@ ap_status launch_mm(const DeviceInfo& di, const MatmulParams& P, const MatmulArg
 
 ap_status launch_matmul_fp8(const DeviceInfo& di, const Options& o, const MatmulArgs& a, cudaStream_t stream) {
     const int64_t size = a.c_type == AP_F32 ? 4 : 2;
-    if (a.k == 0) {
-        return cudaMemset2DAsync(a.c, static_cast<size_t>(a.ldc * size), 0, static_cast<size_t>(a.n * size),
-                                 static_cast<size_t>(a.m), stream) == cudaSuccess
-                   ? AP_OK
-                   : AP_ERR_CUDA;
+    if (a.k == 0) {  // all zeros
+        const size_t pitch = static_cast<size_t>(a.ldc * size), width = static_cast<size_t>(a.n * size);
+        if (pitch <= INT32_MAX)  // the largest pitch that a 2-D call takes
+            return cudaMemset2DAsync(a.c, pitch, 0, width, static_cast<size_t>(a.m), stream) == cudaSuccess ? AP_OK : AP_ERR_CUDA;
+        for (int64_t i = 0; i < a.m; ++i)
+            if (cudaMemsetAsync(static_cast<char*>(a.c) + i * pitch, 0, width, stream) != cudaSuccess) return AP_ERR_CUDA;
+        return AP_OK;
     }
     MatmulParams P{};
     P.c = a.c;
