@@ -10,15 +10,16 @@ namespace {
 
 struct NormParams {
     NormArgs a;
-    bool vec_x, vec_r, vec_y, vec_q, vec_w;  // 16-byte (codes: 8-byte) aligned rows
+    bool vec_x, vec_r, vec_y, vec_q, vec_w;  // 16-byte (codes: 8-byte) aligned rows (of rows too wide for registers)
     int64_t blocks;                          // scales of a row
 };
 
 // What is written of a row's y, C chunks a thread `step` columns apart, the
-// first at col. The 16 lanes of a half warp hold one block of 128, so a
-// block's amax is four shuffles away; the chunks' shuffles run side by side.
-// WHOLE: chunks are whole or empty and every output is aligned.
-template <typename T, int C, bool WHOLE>
+// first at col. A block's 128 values lie in the 16 lanes of a half warp, its
+// amax four shuffles away (SPREAD: four in each lane of the warp, five
+// shuffles); the chunks' shuffles run side by side. RAGGED: the last chunk may
+// be short and outputs may not be aligned.
+template <typename T, int C, bool SPREAD, bool RAGGED = false>
 __device__ __forceinline__ void write_row(const NormParams& P, int64_t row, int64_t col, int64_t step, const float (&y)[C][8]) {
     const NormArgs& a = P.a;
     const int64_t left = a.cols - col;
@@ -27,66 +28,95 @@ __device__ __forceinline__ void write_row(const NormParams& P, int64_t row, int6
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             if (left <= c * step) continue;
-            if (WHOLE)
-                store8(out + c * step, y[c]);
-            else
+            if (RAGGED)
                 store8(out + c * step, P.vec_y, left - c * step, y[c]);
+            else
+                put<SPREAD>(out + c * step, static_cast<int>(left - c * step), y[c]);
         }
     }
     if (a.q != nullptr) {
         uint8_t* out = a.q + (row * a.ldq + col);
-        float* scales = a.q_scales + (row * P.blocks + col / kScaleBlock);
-        float m[C];
-#pragma unroll
-        for (int c = 0; c < C; ++c) m[c] = amax8(y[c]);
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1)
-#pragma unroll
-            for (int c = 0; c < C; ++c) m[c] = max_nan(m[c], __shfl_xor_sync(0xffffffffu, m[c], o));
+        constexpr int kPer = SPREAD ? 2 : 1;  // blocks that a thread has values of
+        float m[C][kPer];
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            if (left <= c * step) continue;
-            const Scale s = scale_of(m[c]);
-            const uint2 w = codes8(y[c], s.inv);
-            if (WHOLE)
-                *reinterpret_cast<uint2*>(out + c * step) = w;
-            else
-                store_codes(out + c * step, P.vec_q, left - c * step, w);
-            if ((threadIdx.x & 15) == 0) scales[c * step / kScaleBlock] = s.s;
+            if (SPREAD) {
+                m[c][0] = amax3(amax3(y[c][0], y[c][1], y[c][2]), y[c][3], 0.0f);
+                m[c][kPer - 1] = amax3(amax3(y[c][4], y[c][5], y[c][6]), y[c][7], 0.0f);
+            } else {
+                m[c][0] = amax8(y[c]);
+            }
+        }
+#pragma unroll
+        for (int o = SPREAD ? 16 : 8; o > 0; o >>= 1)
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int b = 0; b < kPer; ++b) m[c][b] = max_nan(m[c][b], __shfl_xor_sync(0xffffffffu, m[c][b], o));
+        if (SPREAD) {
+            const int lane = threadIdx.x & 31;
+            float* scales = a.q_scales + (row * P.blocks + (col - lane) / kScaleBlock);
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                if (left <= c * step) continue;
+                const Scale s0 = scale_of(m[c][0]), s1 = scale_of(m[c][kPer - 1]);
+                float t[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) t[i] = y[c][i] * (i < 4 ? s0.inv : s1.inv);
+                const uint2 w = codes8(t, 1.0f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (c * step + 32 * i < left)
+                        out[c * step + 32 * i] = static_cast<uint8_t>((i < 4 ? w.x >> (8 * i) : w.y >> (8 * (i - 4))) & 0xffu);
+                if (lane == 0) {
+                    scales[c * step / kScaleBlock] = s0.s;
+                    if (left > c * step + kScaleBlock) scales[c * step / kScaleBlock + 1] = s1.s;
+                }
+            }
+        } else {
+            float* scales = a.q_scales + (row * P.blocks + col / kScaleBlock);
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                if (left <= c * step) continue;
+                const Scale s = scale_of(m[c][0]);
+                const uint2 w = codes8(y[c], s.inv);
+                if (RAGGED)
+                    store_codes(out + c * step, P.vec_q, left - c * step, w);
+                else
+                    *reinterpret_cast<uint2*>(out + c * step) = w;
+                if ((threadIdx.x & 15) == 0) scales[c * step / kScaleBlock] = s.s;
+            }
         }
     }
 }
 
 // One row a CTA (WARP: a warp), C chunks of eight elements a thread.
-template <typename T, typename R, int C, bool WARP>
+template <typename T, typename R, int C, bool WARP, bool SPREAD>
 __global__ void __launch_bounds__(WARP ? 256 : 1024) rms_norm_kernel(const __grid_constant__ NormParams P) {
     __shared__ float scratch[32];
     ptx::let_next_grid_start();
     ptx::wait_previous_grid();
     const NormArgs& a = P.a;
-    const int lane = WARP ? threadIdx.x & 31 : threadIdx.x;
-    const int width = WARP ? 32 : blockDim.x;
+    const int me = WARP ? threadIdx.x & 31 : threadIdx.x;  // in the row
+    const int apart = 8 * (WARP ? 32 : blockDim.x);        // columns between a thread's chunks
     const int64_t row = WARP ? static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
     if (WARP && row >= a.rows) return;
-    const T* x = static_cast<const T*>(a.x) + row * a.ldx;
+    const int col = first_column<SPREAD>(me), left = static_cast<int>(a.cols) - col;
+    const T* x = static_cast<const T*>(a.x) + (row * a.ldx + col);
     float h[C][8];
     float sum = 0.0f;
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-        const int64_t col = 8 * static_cast<int64_t>(c * width + lane);
-        load8(x + col, P.vec_x, a.cols - col).unpack(h[c]);
-    }
+    for (int c = 0; c < C; ++c) take<SPREAD>(x + c * apart, left - c * apart, h[c]);
     if (a.residual != nullptr) {
-        const R* r = static_cast<const R*>(a.residual) + row * a.ldr;
-        R* out = static_cast<R*>(a.residual_out) + row * a.ldr;
+        const R* r = static_cast<const R*>(a.residual) + (row * a.ldr + col);
+        R* out = static_cast<R*>(a.residual_out) + (row * a.ldr + col);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const int64_t col = 8 * static_cast<int64_t>(c * width + lane);
             float v[8];
-            load8(r + col, P.vec_r, a.cols - col).unpack(v);
+            take<SPREAD>(r + c * apart, left - c * apart, v);
 #pragma unroll
             for (int i = 0; i < 8; ++i) h[c][i] += v[i];
-            if (col < a.cols) store8(out + col, P.vec_r, a.cols - col, h[c]);
+            put<SPREAD>(out + c * apart, left - c * apart, h[c]);
         }
     }
 #pragma unroll
@@ -95,21 +125,20 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) rms_norm_kernel(const __gri
         for (int i = 0; i < 8; ++i) sum = fmaf(h[c][i], h[c][i], sum);
     sum = row_sum<WARP>(sum, scratch);
     const float r = __frcp_rn(__fsqrt_rn(__fdiv_rn(sum, static_cast<float>(a.cols)) + a.eps));
-    if (a.rstd != nullptr && lane == 0) a.rstd[row] = r;
+    if (a.rstd != nullptr && me == 0) a.rstd[row] = r;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-        const int64_t col = 8 * static_cast<int64_t>(c * width + lane);
         float w[8];
-        load_weight<T>(a.weight, a.weight_type == a.type, P.vec_w, col, a.cols - col, w);
+        take_weight<SPREAD, T>(a.weight, a.weight_type == a.type, col + c * apart, left - c * apart, w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) h[c][i] *= r * w[i];
     }
-    write_row<T, C, false>(P, row, 8 * lane, 8 * width, h);
+    write_row<T, C, SPREAD>(P, row, col, apart, h);
 }
 
 // The ring's form: teams of warps, rows from shared memory, the weight in
 // registers for the whole grid's life (four chunks: in shared memory).
-template <typename T, typename R, int C, bool RES, Weights W>
+template <typename T, typename R, int C, bool RES, Weights W, bool SPREAD>
 __global__ void __launch_bounds__(kRingThreads, 1)
     rms_norm_ring_kernel(const __grid_constant__ NormParams P, const __grid_constant__ RowRing ring) {
     extern __shared__ __align__(128) unsigned char smem[];
@@ -130,15 +159,12 @@ __global__ void __launch_bounds__(kRingThreads, 1)
     if (team >= ring.teams) return;
     const int me = threadIdx.x - team * width;
     const int apart = 8 * width;  // columns between a thread's chunks
-    const int left = static_cast<int>(a.cols) - 8 * me;
+    const int col = first_column<SPREAD>(me), left = static_cast<int>(a.cols) - col;
     float w[kKeep ? C : 1][8];
     if (kKeep) {
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) w[kKeep ? c : 0][i] = 0.0f;
-            if (left > c * apart) load_weight<T>(a.weight, a.weight_type == a.type, 8 * me + c * apart, w[kKeep ? c : 0]);
-        }
+        for (int c = 0; c < C; ++c)
+            take_weight<SPREAD, T>(a.weight, a.weight_type == a.type, col + c * apart, left - c * apart, w[kKeep ? c : 0]);
     }
     const float inv = __frcp_rn(static_cast<float>(a.cols));
     const int64_t step = ring.together * ring.turns;
@@ -158,17 +184,15 @@ __global__ void __launch_bounds__(kRingThreads, 1)
             const bool mine = row < a.rows;  // the same for the whole team
             float h[C][8];
             if (mine) {
-                const T* x = reinterpret_cast<const T*>(stage + slot * ring.bytes[0]) + 8 * me;
-                const R* res = reinterpret_cast<const R*>(stage + ring.offset[1] + slot * ring.bytes[1]) + 8 * me;
+                const T* x = reinterpret_cast<const T*>(stage + row_place<SPREAD>(ring, 0, base, slot)) + col;
+                const R* res = RES ? reinterpret_cast<const R*>(stage + ring.offset[1] + row_place<SPREAD>(ring, 1, base, slot)) + col
+                                   : nullptr;
 #pragma unroll
                 for (int c = 0; c < C; ++c) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) h[c][i] = 0.0f;
-                    if (left <= c * apart) continue;
-                    load8(x + c * apart).unpack(h[c]);
-                    if (RES) {
+                    take<SPREAD>(x + c * apart, left - c * apart, h[c]);
+                    if (RES && left > c * apart) {
                         float v[8];
-                        load8(res + c * apart).unpack(v);
+                        take<SPREAD>(res + c * apart, left - c * apart, v);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) h[c][i] += v[i];
                     }
@@ -185,10 +209,9 @@ __global__ void __launch_bounds__(kRingThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) sum = fmaf(h[c][i], h[c][i], sum);
             if (RES) {
-                R* out = static_cast<R*>(a.residual_out) + (row * a.ldr + 8 * me);
+                R* out = static_cast<R*>(a.residual_out) + (row * a.ldr + col);
 #pragma unroll
-                for (int c = 0; c < C; ++c)
-                    if (left > c * apart) store8(out + c * apart, h[c]);
+                for (int c = 0; c < C; ++c) put<SPREAD>(out + c * apart, left - c * apart, h[c]);
             }
             sum = team_sum(sum, &scratch[turn][team * ring.team_warps], team, ring.team_warps);
             const float r = __frcp_rn(__fsqrt_rn(fmaf(sum, inv, a.eps)));
@@ -196,12 +219,12 @@ __global__ void __launch_bounds__(kRingThreads, 1)
 #pragma unroll
             for (int c = 0; c < C; ++c) {
                 float again[8];
-                if (!kKeep && left > c * apart) again_weight<T, W>(P, weights, 8 * me + c * apart, again);
+                if (!kKeep && left > c * apart) again_weight<T, W, SPREAD>(P, weights, col + c * apart, left - c * apart, again);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     if (kKeep || left > c * apart) h[c][i] *= r * (kKeep ? w[kKeep ? c : 0][i] : again[i]);
             }
-            write_row<T, C, true>(P, row, 8 * me, apart, h);
+            write_row<T, C, SPREAD>(P, row, col, apart, h);
         }
         s += groups;
         while (s >= ring.stages) s -= ring.stages, ++round;
@@ -247,35 +270,39 @@ __global__ void __launch_bounds__(1024) rms_norm_wide_kernel(const __grid_consta
         load_h(col, h[0]);
         if (res != nullptr && col < a.cols)
             store8(static_cast<R*>(a.residual_out) + row * a.ldr + col, P.vec_r, a.cols - col, h[0]);
-        load_weight<T>(a.weight, a.weight_type == a.type, P.vec_w, col, a.cols - col, w);
+        if (a.weight_type == a.type)
+            load8(static_cast<const T*>(a.weight) + col, P.vec_w, a.cols - col).unpack(w);
+        else
+            load8(static_cast<const float*>(a.weight) + col, P.vec_w, a.cols - col).unpack(w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) h[0][i] *= r * w[i];
-        write_row<T, 1, false>(P, row, col, 0, h);
+        write_row<T, 1, false, true>(P, row, col, 0, h);
     }
 }
 
 template <typename T, typename R, int C, bool WARP>
-ap_status launch_norm_c(const NormParams& P, cudaStream_t stream) {
+ap_status launch_norm_c(const NormParams& P, bool whole, cudaStream_t stream) {
     const int64_t chunks = (P.a.cols + 7) / 8;
     const int threads = WARP ? 256 : static_cast<int>(((chunks + C - 1) / C + 31) / 32 * 32);
     const int64_t grid = WARP ? (P.a.rows + 7) / 8 : P.a.rows;
     if (grid >= kMaxGrid) return AP_ERR_SHAPE;
-    record_launch(PATH_NORM, grid, 8 * C, 0, 0, WARP ? 1 : 0);
-    return launch_early(rms_norm_kernel<T, R, C, WARP>, grid, threads, stream, P);
+    record_launch(PATH_NORM, grid, 8 * C, 0, 0, (WARP ? 1 : 0) | (whole ? 0 : 8));
+    return whole ? launch_early(rms_norm_kernel<T, R, C, WARP, false>, grid, threads, stream, P)
+                 : launch_early(rms_norm_kernel<T, R, C, WARP, true>, grid, threads, stream, P);
 }
 
-template <typename T, typename R, bool RES>
+template <typename T, typename R, bool RES, bool SPREAD>
 ap_status launch_norm_ring(const DeviceInfo& di, const NormParams& P, const RowRing& ring, cudaStream_t stream) {
     static std::atomic<int> configured[5][64];
     if (ring.chunks == 2)
-        return launch_ring_kernel(di, rms_norm_ring_kernel<T, R, 2, RES, IN_REGISTERS>, configured[0], P, ring, PATH_NORM, stream);
+        return launch_ring_kernel(di, rms_norm_ring_kernel<T, R, 2, RES, IN_REGISTERS, SPREAD>, configured[0], P, ring, PATH_NORM, stream);
     if (ring.chunks == 3)
         return ring.keep_weights
-                   ? launch_ring_kernel(di, rms_norm_ring_kernel<T, R, 3, RES, IN_SHARED>, configured[1], P, ring, PATH_NORM, stream)
-                   : launch_ring_kernel(di, rms_norm_ring_kernel<T, R, 3, RES, IN_L2>, configured[2], P, ring, PATH_NORM, stream);
+                   ? launch_ring_kernel(di, rms_norm_ring_kernel<T, R, 3, RES, IN_SHARED, SPREAD>, configured[1], P, ring, PATH_NORM, stream)
+                   : launch_ring_kernel(di, rms_norm_ring_kernel<T, R, 3, RES, IN_L2, SPREAD>, configured[2], P, ring, PATH_NORM, stream);
     return ring.keep_weights
-               ? launch_ring_kernel(di, rms_norm_ring_kernel<T, R, 4, RES, IN_SHARED>, configured[3], P, ring, PATH_NORM, stream)
-               : launch_ring_kernel(di, rms_norm_ring_kernel<T, R, 4, RES, IN_L2>, configured[4], P, ring, PATH_NORM, stream);
+               ? launch_ring_kernel(di, rms_norm_ring_kernel<T, R, 4, RES, IN_SHARED, SPREAD>, configured[3], P, ring, PATH_NORM, stream)
+               : launch_ring_kernel(di, rms_norm_ring_kernel<T, R, 4, RES, IN_L2, SPREAD>, configured[4], P, ring, PATH_NORM, stream);
 }
 
 // The ring's set-up is paid back from this many elements on (1216 x 4096: 8.2
@@ -298,16 +325,19 @@ ap_status launch_norm_t(const DeviceInfo& di, const Options& o, const NormArgs& 
     const void* const in[] = {a.x, a.residual};
     const int64_t ld[] = {a.ldx, a.ldr}, size[] = {sizeof(T), sizeof(R)};
     const bool res = a.residual != nullptr;
-    const bool whole = (!res || P.vec_r) && P.vec_w && (a.y == nullptr || P.vec_y) && (a.q == nullptr || P.vec_q);
+    const bool whole =
+        a.cols % 8 == 0 && P.vec_x && (!res || P.vec_r) && P.vec_w && (a.y == nullptr || P.vec_y) && (a.q == nullptr || P.vec_q);
     const bool many = o.force_path == 1 || (o.force_path != 2 && a.cols > kRingColumns && a.rows >= kRingElements / a.cols);
-    if (many && whole && plan_ring(di, o, &ring, res ? 2 : 1, in, ld, size, nullptr, a.rows, a.cols)) {
-        return res ? launch_norm_ring<T, R, true>(di, P, ring, stream) : launch_norm_ring<T, T, false>(di, P, ring, stream);
+    if (many && plan_ring(di, o, &ring, res ? 2 : 1, in, ld, size, nullptr, a.rows, a.cols, whole)) {
+        if (whole)
+            return res ? launch_norm_ring<T, R, true, false>(di, P, ring, stream) : launch_norm_ring<T, T, false, false>(di, P, ring, stream);
+        return res ? launch_norm_ring<T, R, true, true>(di, P, ring, stream) : launch_norm_ring<T, T, false, true>(di, P, ring, stream);
     }
-    if (a.cols <= 256) return launch_norm_c<T, R, 1, true>(P, stream);
-    if (a.cols <= 512) return launch_norm_c<T, R, 2, true>(P, stream);
-    if (a.cols <= 4096) return launch_norm_c<T, R, 1, false>(P, stream);
-    if (a.cols <= 8192) return launch_norm_c<T, R, 2, false>(P, stream);
-    if (a.cols <= 32768) return launch_norm_c<T, R, 4, false>(P, stream);
+    if (a.cols <= 256) return launch_norm_c<T, R, 1, true>(P, whole, stream);
+    if (a.cols <= 512) return launch_norm_c<T, R, 2, true>(P, whole, stream);
+    if (a.cols <= 4096) return launch_norm_c<T, R, 1, false>(P, whole, stream);
+    if (a.cols <= 8192) return launch_norm_c<T, R, 2, false>(P, whole, stream);
+    if (a.cols <= 32768) return launch_norm_c<T, R, 4, false>(P, whole, stream);
     if (a.rows >= kMaxGrid) return AP_ERR_SHAPE;
     record_launch(PATH_NORM, a.rows, 0, 0, 0, 2);
     return launch_early(rms_norm_wide_kernel<T, R>, a.rows, 1024, stream, P);

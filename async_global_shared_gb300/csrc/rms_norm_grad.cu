@@ -10,13 +10,12 @@ namespace {
 
 struct GradParams {
     NormGradArgs a;
-    bool vec_dy, vec_h, vec_r, vec_dx, vec_w;
 };
 
 // CTA b takes rows b, b + grid, ...; a thread keeps its columns' share of
 // dweight in registers and writes it to the CTA's row of the workspace at the
 // end, so the sum's order depends on the sizes alone.
-template <typename T, typename R, int C>
+template <typename T, typename R, int C, bool SPREAD>
 __global__ void __launch_bounds__(512) rms_norm_grad_kernel(const __grid_constant__ GradParams P) {
     __shared__ float scratch[2][32];
     ptx::let_next_grid_start();
@@ -28,6 +27,7 @@ __global__ void __launch_bounds__(512) rms_norm_grad_kernel(const __grid_constan
 #pragma unroll
         for (int i = 0; i < 8; ++i) dw[c][i] = 0.0f;
     const float inv = __frcp_rn(static_cast<float>(a.cols));
+    const int first = first_column<SPREAD>(threadIdx.x), apart = 8 * blockDim.x, cols = static_cast<int>(a.cols);
     int turn = 0;  // two scratch rows in turn: one barrier a row is enough
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
         const T* dy = static_cast<const T*>(a.dy) + row * a.lddy;
@@ -37,11 +37,11 @@ __global__ void __launch_bounds__(512) rms_norm_grad_kernel(const __grid_constan
         float sum = 0.0f;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const int64_t col = 8 * static_cast<int64_t>(c * blockDim.x + threadIdx.x);
+            const int col = first + c * apart;
             float w[8];
-            load8(dy + col, P.vec_dy, a.cols - col).unpack(g[c]);
-            load8(h + col, P.vec_h, a.cols - col).unpack(n[c]);
-            load_weight<T>(a.weight, a.weight_type == a.type, P.vec_w, col, a.cols - col, w);
+            take<SPREAD>(dy + col, cols - col, g[c]);
+            take<SPREAD>(h + col, cols - col, n[c]);
+            take_weight<SPREAD, T>(a.weight, a.weight_type == a.type, col, cols - col, w);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 n[c][i] *= r;
@@ -53,31 +53,30 @@ __global__ void __launch_bounds__(512) rms_norm_grad_kernel(const __grid_constan
         const float mean = row_sum<false>(sum, scratch[turn]) * inv;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const int64_t col = 8 * static_cast<int64_t>(c * blockDim.x + threadIdx.x);
-            if (col >= a.cols) continue;
+            const int col = first + c * apart;
+            if (col >= cols) continue;
 #pragma unroll
             for (int i = 0; i < 8; ++i) g[c][i] = fmaf(-n[c][i], mean, g[c][i]);
             float d[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            if (a.dresidual != nullptr)
-                load8(static_cast<const R*>(a.dresidual) + row * a.lddr + col, P.vec_r, a.cols - col).unpack(d);
+            if (a.dresidual != nullptr) take<SPREAD>(static_cast<const R*>(a.dresidual) + row * a.lddr + col, cols - col, d);
 #pragma unroll
             for (int i = 0; i < 8; ++i) g[c][i] = fmaf(r, g[c][i], d[i]);
-            store8(static_cast<R*>(a.dx) + row * a.lddx + col, P.vec_dx, a.cols - col, g[c]);
+            put<SPREAD>(static_cast<R*>(a.dx) + row * a.lddx + col, cols - col, g[c]);
         }
     }
     if (a.dweight == nullptr) return;
     float* part = a.workspace + static_cast<int64_t>(blockIdx.x) * a.cols;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-        const int64_t col = 8 * static_cast<int64_t>(c * blockDim.x + threadIdx.x);
-        if (col < a.cols) store8(part + col, a.cols % 4 == 0, a.cols - col, dw[c]);
+        const int col = first + c * apart;
+        put<SPREAD>(part + col, cols - col, dw[c]);
     }
 }
 
 // The ring's form: teams of warps, rows and their rstd from shared memory. A
 // thread's columns are the same for every row, so it keeps their weights (four
 // chunks: in shared memory) and their share of dweight in registers.
-template <typename T, typename R, int C, bool RES, Weights W>
+template <typename T, typename R, int C, bool RES, Weights W, bool SPREAD>
 __global__ void __launch_bounds__(kRingThreads, 1)
     rms_norm_grad_ring_kernel(const __grid_constant__ GradParams P, const __grid_constant__ RowRing ring) {
     extern __shared__ __align__(128) unsigned char smem[];
@@ -98,13 +97,13 @@ __global__ void __launch_bounds__(kRingThreads, 1)
     const int team = warp / ring.team_warps, width = 32 * ring.team_warps;
     if (team >= ring.teams) return;
     const int me = threadIdx.x - team * width;
-    const int cols = static_cast<int>(a.cols);  // a multiple of 8
+    const int first = first_column<SPREAD>(me), apart = 8 * width, cols = static_cast<int>(a.cols);
     float w[kKeep ? C : 1][8];
     if (kKeep) {
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const int col = 8 * (c * width + me);
-            if (col < cols) load_weight<T>(a.weight, same, col, w[kKeep ? c : 0]);
+            const int col = first + c * apart;
+            if (col < cols) take_weight<SPREAD, T>(a.weight, same, col, cols - col, w[kKeep ? c : 0]);
         }
     }
     float dw[C][8];
@@ -131,18 +130,18 @@ __global__ void __launch_bounds__(kRingThreads, 1)
             if (mine) {
                 // the row is read from shared memory again after its sum: that
                 // is cheaper than the registers it would take
-                const T* p = reinterpret_cast<const T*>(stage + slot * ring.bytes[0]);
-                const R* q = reinterpret_cast<const R*>(stage + ring.offset[1] + slot * ring.bytes[1]);
+                const T* p = reinterpret_cast<const T*>(stage + row_place<SPREAD>(ring, 0, base, slot));
+                const R* q = reinterpret_cast<const R*>(stage + ring.offset[1] + row_place<SPREAD>(ring, 1, base, slot));
                 const float r = reinterpret_cast<const float*>(stage + ring.side_offset)[slot];
                 float sum = 0.0f;
 #pragma unroll
                 for (int c = 0; c < C; ++c) {
-                    const int col = 8 * (c * width + me);
+                    const int col = first + c * apart;
                     if (col >= cols) continue;
                     float g[8], n[8], again[8];
-                    load8(p + col).unpack(g);
-                    load8(q + col).unpack(n);
-                    if (!kKeep) again_weight<T, W>(P, weights, col, again);
+                    take<SPREAD>(p + col, cols - col, g);
+                    take<SPREAD>(q + col, cols - col, n);
+                    if (!kKeep) again_weight<T, W, SPREAD>(P, weights, col, cols - col, again);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         n[i] *= r;
@@ -153,19 +152,21 @@ __global__ void __launch_bounds__(kRingThreads, 1)
                 const float mean = team_sum(sum, &scratch[turn][team * ring.team_warps], team, ring.team_warps) * inv;
 #pragma unroll
                 for (int c = 0; c < C; ++c) {
-                    const int col = 8 * (c * width + me);
+                    const int col = first + c * apart;
                     if (col >= cols) continue;
                     float g[8], n[8], d[8] = {0, 0, 0, 0, 0, 0, 0, 0}, again[8];
-                    load8(p + col).unpack(g);
-                    load8(q + col).unpack(n);
-                    if (RES) load8(reinterpret_cast<const R*>(stage + ring.offset[2] + slot * ring.bytes[2]) + col).unpack(d);
-                    if (!kKeep) again_weight<T, W>(P, weights, col, again);
+                    take<SPREAD>(p + col, cols - col, g);
+                    take<SPREAD>(q + col, cols - col, n);
+                    if (RES)
+                        take<SPREAD>(reinterpret_cast<const R*>(stage + ring.offset[2] + row_place<SPREAD>(ring, 2, base, slot)) + col,
+                                     cols - col, d);
+                    if (!kKeep) again_weight<T, W, SPREAD>(P, weights, col, cols - col, again);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const float gw = g[i] * (kKeep ? w[kKeep ? c : 0][i] : again[i]);
                         g[i] = fmaf(r, fmaf(-(n[i] * r), mean, gw), d[i]);
                     }
-                    store8(static_cast<R*>(a.dx) + row * a.lddx + col, g);
+                    put<SPREAD>(static_cast<R*>(a.dx) + row * a.lddx + col, cols - col, g);
                 }
             }
         }
@@ -184,8 +185,8 @@ __global__ void __launch_bounds__(kRingThreads, 1)
         ptx::named_barrier_sync(15, all);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const int col = 8 * (c * width + me);
-            if (col < cols) store8(shares + team * cols + col, dw[c]);
+            const int col = first + c * apart;
+            put<SPREAD>(shares + team * cols + col, cols - col, dw[c]);
         }
         ptx::named_barrier_sync(15, all);
         for (int col = threadIdx.x; col < cols; col += all) {
@@ -196,8 +197,8 @@ __global__ void __launch_bounds__(kRingThreads, 1)
     } else {
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const int col = 8 * (c * width + me);
-            if (col < cols) store8(part + col, dw[c]);
+            const int col = first + c * apart;
+            put<SPREAD>(part + col, cols - col, dw[c]);
         }
     }
 }
@@ -261,53 +262,55 @@ __global__ void __launch_bounds__(256) sum_partials_kernel(const float* part, fl
 constexpr int64_t kGradSMs = 152;  // the partials' number is part of the interface (workspace size), so no device query
 
 template <typename T, typename R, int C>
-ap_status run_grad(const GradParams& P, int64_t grid, cudaStream_t stream) {
+ap_status run_grad(const GradParams& P, bool whole, int64_t grid, cudaStream_t stream) {
     const int64_t chunks = (P.a.cols + 7) / 8;
     const int threads = static_cast<int>(((chunks + C - 1) / C + 31) / 32 * 32);
-    record_launch(PATH_NORM_GRAD, grid, 8 * C, 0, 0, 0);
-    return launch_early(rms_norm_grad_kernel<T, R, C>, grid, threads, stream, P);
+    record_launch(PATH_NORM_GRAD, grid, 8 * C, 0, 0, whole ? 0 : 8);
+    return whole ? launch_early(rms_norm_grad_kernel<T, R, C, false>, grid, threads, stream, P)
+                 : launch_early(rms_norm_grad_kernel<T, R, C, true>, grid, threads, stream, P);
 }
 
-template <typename T, typename R, bool RES>
+template <typename T, typename R, bool RES, bool SPREAD>
 ap_status launch_grad_ring(const DeviceInfo& di, const GradParams& P, const RowRing& ring, cudaStream_t stream) {
     static std::atomic<int> configured[5][64];
     if (ring.chunks == 2)
-        return launch_ring_kernel(di, rms_norm_grad_ring_kernel<T, R, 2, RES, IN_REGISTERS>, configured[0], P, ring, PATH_NORM_GRAD, stream);
+        return launch_ring_kernel(di, rms_norm_grad_ring_kernel<T, R, 2, RES, IN_REGISTERS, SPREAD>, configured[0], P, ring, PATH_NORM_GRAD, stream);
     if (ring.chunks == 3)
         return ring.keep_weights
-                   ? launch_ring_kernel(di, rms_norm_grad_ring_kernel<T, R, 3, RES, IN_SHARED>, configured[1], P, ring, PATH_NORM_GRAD, stream)
-                   : launch_ring_kernel(di, rms_norm_grad_ring_kernel<T, R, 3, RES, IN_L2>, configured[2], P, ring, PATH_NORM_GRAD, stream);
+                   ? launch_ring_kernel(di, rms_norm_grad_ring_kernel<T, R, 3, RES, IN_SHARED, SPREAD>, configured[1], P, ring, PATH_NORM_GRAD, stream)
+                   : launch_ring_kernel(di, rms_norm_grad_ring_kernel<T, R, 3, RES, IN_L2, SPREAD>, configured[2], P, ring, PATH_NORM_GRAD, stream);
     return ring.keep_weights
-               ? launch_ring_kernel(di, rms_norm_grad_ring_kernel<T, R, 4, RES, IN_SHARED>, configured[3], P, ring, PATH_NORM_GRAD, stream)
-               : launch_ring_kernel(di, rms_norm_grad_ring_kernel<T, R, 4, RES, IN_L2>, configured[4], P, ring, PATH_NORM_GRAD, stream);
+               ? launch_ring_kernel(di, rms_norm_grad_ring_kernel<T, R, 4, RES, IN_SHARED, SPREAD>, configured[3], P, ring, PATH_NORM_GRAD, stream)
+               : launch_ring_kernel(di, rms_norm_grad_ring_kernel<T, R, 4, RES, IN_L2, SPREAD>, configured[4], P, ring, PATH_NORM_GRAD, stream);
 }
 
 template <typename T, typename R>
 ap_status launch_grad_t(const DeviceInfo& di, const Options& o, const NormGradArgs& a, cudaStream_t stream) {
     GradParams P;
     P.a = a;
-    P.vec_dy = rows_aligned(a.dy, a.lddy, sizeof(T), 16);
-    P.vec_h = rows_aligned(a.h, a.ldh, sizeof(R), 16);
-    P.vec_r = rows_aligned(a.dresidual, a.lddr, sizeof(R), 16);
-    P.vec_dx = rows_aligned(a.dx, a.lddx, sizeof(R), 16);
-    P.vec_w = reinterpret_cast<uintptr_t>(a.weight) % 16 == 0;
     int64_t grid = norm_grad_partials(a.rows, a.cols);
     RowRing ring;
     const void* const in[] = {a.dy, a.h, a.dresidual};
     const int64_t ld[] = {a.lddy, a.ldh, a.lddr}, size[] = {sizeof(T), sizeof(R), sizeof(R)};
     const bool res = a.dresidual != nullptr;
+    const bool whole = a.cols % 8 == 0 && rows_aligned(a.dy, a.lddy, sizeof(T), 16) && rows_aligned(a.h, a.ldh, sizeof(R), 16) &&
+                       (!res || rows_aligned(a.dresidual, a.lddr, sizeof(R), 16)) && rows_aligned(a.dx, a.lddx, sizeof(R), 16) &&
+                       reinterpret_cast<uintptr_t>(a.weight) % 16 == 0;
     if (grid > 0) {
         ap_status st;
-        if (P.vec_dx && P.vec_w && plan_ring(di, o, &ring, res ? 3 : 2, in, ld, size, a.rstd, a.rows, a.cols)) {
+        if (plan_ring(di, o, &ring, res ? 3 : 2, in, ld, size, a.rstd, a.rows, a.cols, whole)) {
             grid = ring_grid(ring, kGradSMs);
-            st = res ? launch_grad_ring<T, R, true>(di, P, ring, stream) : launch_grad_ring<T, R, false>(di, P, ring, stream);
+            if (whole)
+                st = res ? launch_grad_ring<T, R, true, false>(di, P, ring, stream) : launch_grad_ring<T, R, false, false>(di, P, ring, stream);
+            else
+                st = res ? launch_grad_ring<T, R, true, true>(di, P, ring, stream) : launch_grad_ring<T, R, false, true>(di, P, ring, stream);
         } else {
             if (a.cols <= 4096) {
-                st = run_grad<T, R, 1>(P, grid, stream);
+                st = run_grad<T, R, 1>(P, whole, grid, stream);
             } else if (a.cols <= 8192) {
-                st = run_grad<T, R, 2>(P, grid, stream);
+                st = run_grad<T, R, 2>(P, whole, grid, stream);
             } else if (a.cols <= 16384) {
-                st = run_grad<T, R, 4>(P, grid, stream);
+                st = run_grad<T, R, 4>(P, whole, grid, stream);
             } else {
                 record_launch(PATH_NORM_GRAD, grid, 0, 0, 0, 2);
                 st = launch_early(rms_norm_grad_wide_kernel<T, R>, grid, 1024, stream, P);

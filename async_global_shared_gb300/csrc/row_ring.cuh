@@ -25,19 +25,44 @@ __device__ __forceinline__ float row_sum(float v, float* scratch) {
     return warp_sum(v);
 }
 
-template <typename T>
-__device__ __forceinline__ void load_weight(const void* w, bool same, int64_t col, float (&v)[8]) {
-    if (same)
-        load8(static_cast<const T*>(w) + col).unpack(v);
-    else
-        load8(static_cast<const float*>(w) + col).unpack(v);
+// How a warp's 256 columns of a row lie in its threads, eight elements each.
+// Whole rows (every matrix's rows on 16-byte boundaries, a multiple of eight
+// columns): lane l has columns 8 l .. 8 l + 7 and moves them 16 bytes at a
+// time. SPREAD, for all others: columns l, l + 32, ..., so that a warp's access
+// to single elements still is one run of memory. (8287 x 166 floats: gradient
+// 37 us with eight neighbours a thread and plain accesses.)
+template <bool SPREAD>
+__device__ __forceinline__ int first_column(int thread) {
+    return SPREAD ? 8 * (thread & ~31) + (thread & 31) : 8 * thread;
 }
-template <typename T>
-__device__ __forceinline__ void load_weight(const void* w, bool same, bool vec, int64_t col, int64_t n, float (&v)[8]) {
+
+// A thread's eight elements of a row's chunk at p, zeros past the row's end:
+// `left` columns from p's on, p's own among them.
+template <bool SPREAD, typename T>
+__device__ __forceinline__ void take(const T* p, int left, float (&v)[8]) {
+    if (!SPREAD && left > 0) {
+        load8(p).unpack(v);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = SPREAD && 32 * i < left ? to_f32(p[32 * i]) : 0.0f;
+}
+template <bool SPREAD, typename T>
+__device__ __forceinline__ void put(T* p, int left, const float (&v)[8]) {
+    if (!SPREAD) {
+        if (left > 0) store8(p, v);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (32 * i < left) p[32 * i] = from_f32<T>(v[i]);
+}
+template <bool SPREAD, typename T>
+__device__ __forceinline__ void take_weight(const void* w, bool same, int col, int left, float (&v)[8]) {
     if (same)
-        load8(static_cast<const T*>(w) + col, vec, n).unpack(v);
+        take<SPREAD>(static_cast<const T*>(w) + col, left, v);
     else
-        load8(static_cast<const float*>(w) + col, vec, n).unpack(v);
+        take<SPREAD>(static_cast<const float*>(w) + col, left, v);
 }
 
 // ------------------------------------------------------------------ ring of rows
@@ -56,6 +81,12 @@ __device__ __forceinline__ void load_weight(const void* w, bool same, bool vec, 
 // stages to fill. Stage j of a CTA belongs to the teams' group j mod (teams /
 // together) and holds the rows from (j * grid + CTA) * together * turns, turn
 // m's row for the group's team t being m * together + t.
+//
+// A bulk copy moves whole 16-byte units. Rows that do not start or end on such
+// a boundary bring the units they share with their neighbours whole and keep
+// their place in a unit in shared memory; at the first and the last row, where
+// a unit's other bytes may not be the matrix's, the producer moves the row's
+// bytes of it itself.
 constexpr int kRingWarps = 16;
 constexpr int kRingThreads = 32 * (kRingWarps + 1);
 constexpr int kMaxRingStages = 32;
@@ -66,13 +97,14 @@ struct RowRing {
     const unsigned char* in[kMaxInputs];
     int64_t pitch[kMaxInputs];
     uint32_t bytes[kMaxInputs];   // of a row
+    uint32_t apart[kMaxInputs];   // between a stage's rows
     uint32_t offset[kMaxInputs];  // of an input's rows in a stage
     const float* side;      // one float a row as well, or nullptr
     uint32_t side_offset;   // of their places in a stage
     uint32_t weight_offset; // of the weight in floats, past the stages
     uint32_t stage_bytes;
     uint32_t smem;          // all of it
-    bool keep_weights;
+    bool keep_weights, spread;
     int inputs, chunks, team_warps, teams, together, turns, stages;
     int64_t rows;
     uint32_t tx_extra;  // fault injection: bytes every stage waits for in vain
@@ -106,6 +138,38 @@ __device__ __forceinline__ bool ring_wait(const RowRing& R, RingBars& b, uint64_
     return w == WAIT_OK;
 }
 
+// Where a stage's row `slot` of input i lies in the input's part of the stage
+// that starts with row `base`.
+template <bool SPREAD>
+__device__ __forceinline__ uint32_t row_place(const RowRing& R, int i, int64_t base, int slot) {
+    const uint32_t at = slot * R.apart[i];
+    if (!SPREAD) return at;
+    const int64_t row = R.apart[i] == R.bytes[i] ? base : base + slot;
+    return at + (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(R.in[i]) + row * R.pitch[i]) & 15u);
+}
+
+// Brings bytes [from, to) of an input to dst, which has the place in a 16-byte
+// unit that `from` has; [first, last) are the input's own bytes. What the
+// barrier is to expect is told it here, its arrival is the caller's.
+__device__ __forceinline__ void copy_units(uint32_t dst, const unsigned char* from, const unsigned char* to,
+                                           const unsigned char* first, const unsigned char* last, uint32_t bar) {
+    const auto down = [](const unsigned char* p) { return p - (reinterpret_cast<uintptr_t>(p) & 15); };
+    const auto up = [&](const unsigned char* p) { return down(p + 15); };
+    const auto by_hand = [&](const unsigned char* a, const unsigned char* b) {
+        for (; a < b; a += 2)
+            ptx::st_shared_u16(dst + static_cast<uint32_t>(a - from), *reinterpret_cast<const uint16_t*>(a));
+    };
+    const unsigned char* lo = down(from) >= first ? down(from) : up(from);
+    const unsigned char* hi = up(to) <= last ? up(to) : down(to);
+    if (lo >= hi) lo = hi = to;  // no whole unit
+    by_hand(from, lo);
+    if (hi > lo) {
+        by_hand(hi, to);
+        ptx::mbar_expect_tx(bar, static_cast<uint32_t>(hi - lo));
+        ptx::bulk_g2s(dst + static_cast<uint32_t>(lo - from), lo, static_cast<uint32_t>(hi - lo), bar);
+    }
+}
+
 // The producer warp: lane 0 issues the rows' copies, all lanes the side
 // values' (4 bytes each, per-thread asynchronous copies on the same barrier).
 __device__ __forceinline__ void ring_produce(const RowRing& R, RingBars& b, uint32_t smem) {
@@ -123,7 +187,18 @@ __device__ __forceinline__ void ring_produce(const RowRing& R, RingBars& b, uint
         const int n = static_cast<int>(R.rows - row < step ? R.rows - row : step);
         const uint32_t bar = ptx::smem_addr(&b.full[s]);
         const uint32_t stage = smem + s * R.stage_bytes;
-        if (lane == 0) {
+        if (lane == 0 && R.spread) {
+            for (int i = 0; i < R.inputs; ++i) {
+                const unsigned char* src = R.in[i] + row * R.pitch[i];
+                const unsigned char* last = R.in[i] + ((R.rows - 1) * R.pitch[i] + R.bytes[i]);
+                const bool one = R.apart[i] == R.bytes[i];  // rows without gaps: one span
+                for (int k = 0; k < (one ? 1 : n); ++k, src += R.pitch[i])
+                    copy_units(stage + R.offset[i] + row_place<true>(R, i, row, k), src, src + (one ? n : 1) * R.bytes[i], R.in[i],
+                               last, bar);
+            }
+            ptx::fence_proxy_async_smem();  // places filled by hand are copied over later
+            ptx::mbar_arrive_expect_tx(bar, R.tx_extra);
+        } else if (lane == 0) {
             ptx::mbar_arrive_expect_tx(bar, static_cast<uint32_t>(n) * row_bytes + R.tx_extra);
             for (int i = 0; i < R.inputs; ++i) {
                 const uint32_t dst = stage + R.offset[i];
@@ -166,11 +241,12 @@ __device__ __forceinline__ float team_sum(float v, float* scratch, int team, int
 }
 
 // Fill in the plan for rows of `cols` elements; false where the ring does not
-// take these rows (alignment, width). The kernels then move whole chunks only;
-// whether the outputs and the weight allow it is the caller's to check.
+// take these rows (width). whole: the inputs' rows start on 16-byte boundaries
+// and hold a multiple of eight columns.
 bool plan_ring(const DeviceInfo& di, const Options& o, RowRing* R, int inputs, const void* const* in, const int64_t* ld,
-               const int64_t* size, const float* side, int64_t rows, int64_t cols) {
-    if (cols % 8 != 0 || cols > 256 * 4 * kRingWarps) return false;
+               const int64_t* size, const float* side, int64_t rows, int64_t cols, bool whole) {
+    if (cols > 256 * 4 * kRingWarps) return false;
+    R->spread = !whole;
     R->side = side;
     R->tx_extra = static_cast<uint32_t>(o.tx_extra);
     R->timeout_ns = static_cast<uint64_t>(o.timeout_ns);
@@ -179,10 +255,10 @@ bool plan_ring(const DeviceInfo& di, const Options& o, RowRing* R, int inputs, c
     R->rows = rows;
     int64_t row_bytes = 0;
     for (int i = 0; i < inputs; ++i) {
-        if (!rows_aligned(in[i], ld[i], size[i], 16)) return false;
         R->in[i] = static_cast<const unsigned char*>(in[i]);
         R->pitch[i] = ld[i] * size[i];
         R->bytes[i] = static_cast<uint32_t>(cols * size[i]);
+        R->apart[i] = whole || R->pitch[i] == R->bytes[i] ? R->bytes[i] : (R->bytes[i] + 31) / 16 * 16;
         row_bytes += cols * size[i];
     }
     // A thread's chunks of eight elements: what leaves fewest of the 16 warps
@@ -211,7 +287,8 @@ bool plan_ring(const DeviceInfo& di, const Options& o, RowRing* R, int inputs, c
         uint32_t at = 0;
         for (int i = 0; i < inputs; ++i) {
             R->offset[i] = at;
-            at += R->bytes[i] * static_cast<uint32_t>(R->together * R->turns);
+            at += R->apart[i] * static_cast<uint32_t>(R->together * R->turns);
+            if (!whole) at = (at + 31) / 16 * 16;
         }
         R->side_offset = at;
         if (side != nullptr) at += static_cast<uint32_t>(4 * R->together * R->turns + 15) / 16 * 16;
@@ -252,12 +329,12 @@ __device__ __forceinline__ void stage_weights(const void* w, bool same, int64_t 
 enum Weights { IN_REGISTERS, IN_SHARED, IN_L2 };
 
 // Weights of a chunk that are not in registers.
-template <typename T, Weights W, typename Params>
-__device__ __forceinline__ void again_weight(const Params& P, const float* kept, int col, float (&v)[8]) {
+template <typename T, Weights W, bool SPREAD, typename Params>
+__device__ __forceinline__ void again_weight(const Params& P, const float* kept, int col, int left, float (&v)[8]) {
     if (W == IN_SHARED)
-        load8(kept + col).unpack(v);
+        take<SPREAD>(kept + col, left, v);
     else
-        load_weight<T>(P.a.weight, P.a.weight_type == P.a.type, col, v);
+        take_weight<SPREAD, T>(P.a.weight, P.a.weight_type == P.a.type, col, left, v);
 }
 
 constexpr int64_t kMaxGrid = int64_t(1) << 31;
@@ -275,7 +352,7 @@ ap_status launch_ring_kernel(const DeviceInfo& di, K kernel, std::atomic<int> (&
     }
     const int64_t grid = ring_grid(ring, di.sms);
     const size_t smem = ring.smem;
-    record_launch(path, grid, ring.together * ring.turns, static_cast<int64_t>(smem), ring.stages, 4);
+    record_launch(path, grid, ring.together * ring.turns, static_cast<int64_t>(smem), ring.stages, 4 | (ring.spread ? 8 : 0));
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
     cfg.blockDim = dim3(kRingThreads);

@@ -590,6 +590,79 @@ def test_norm_ring_strided_rows_stay_inside(ap, shift, pad):
     fu.check_codes(q.view.clone().view(E4M3), s, yy, 1, rel, "strided ring norm")
 
 
+ODD_SIZES = [(1, 1), (1, 7), (2, 199), (17, 513), (1500, 9), (999, 263), (700, 1001), (311, 2057), (500, 4999), (307, 8201),
+             (40, 16383)]
+
+
+@pytest.mark.parametrize("rows,cols", ODD_SIZES)
+@pytest.mark.parametrize("kind,res,shift,pad", [("f32", "f32", 0, 0), ("bf16", "bf16", 1, 0), ("bf16", "f32", 3, 5), ("f16", None, 0, 0),
+                                                ("f16", "f32", 0, 1)])
+def test_norm_rows_off_the_boundaries(ap, rows, cols, kind, res, shift, pad):
+    """Rows that start and end anywhere, in both forms: what lies around them is neither read into results nor written."""
+    t = TYPES[kind]
+    data = randn(rows, cols, seed=cols).to(t)
+    rdata = None if res is None else (2 * randn(rows, cols, seed=cols + 1)).to(TYPES[res])
+    weight = torch.cat([torch.ones(1, device="cuda"), 1 + 0.1 * randn(cols, seed=2)])[1:]
+    h, rr, yy = fu.norm(f64(data), None if res is None else f64(rdata), f64(weight), 1e-5)
+    rel = (fu.DEPTH / 2 + 8) * U
+    for path in (1, 2):
+        ap.ap_debug_set(ap.AP_DBG_FORCE_PATH, path)
+        x = Strided(rows, cols, t, cols + pad, shift, data)
+        y, q = Strided(rows, cols, t, cols + 2 * pad, 1), Strided(rows, cols, torch.uint8, cols + pad, shift)
+        stream = None if res is None else Strided(rows, cols, TYPES[res], cols + pad, shift, rdata)
+        s, r = torch.empty(rows, fu.blocks(cols), device="cuda"), torch.empty(rows, device="cuda")
+        at = None if res is None else stream.view
+        ap.ap_rms_norm(x.view, weight, 1e-5, y=y.view, q=q.view, q_scales=s, residual=at, residual_out=at, rstd=r)
+        done(ap)
+        assert ap.ap_debug_get(ap.AP_DBG_LAST_FLAGS) in ((12,) if path == 1 and cols <= 8192 else (8, 9, 12))
+        assert all(b.intact() for b in (x, y, q) + (() if res is None else (stream,)))
+        assert torch.equal(x.view, data)
+        assert np.all(np.abs(f64(r) - rr) <= rel * rr)
+        assert np.all(np.abs(f64(y.view) - yy) <= fu.rounding(yy, t) * (1 + rel) + rel * np.abs(yy))
+        if res is not None:
+            assert np.all(np.abs(f64(stream.view) - h) <= fu.rounding(h, TYPES[res]) * (1 + U) + U * np.abs(h))
+        fu.check_codes(q.view.clone().view(E4M3), s, yy, 1, rel, f"norm {rows}x{cols} path {path}")
+        ap.ap_rms_norm(x.view, weight, 1e-5, y=x.view)  # in place
+        done(ap)
+        assert x.intact()
+        if res is None:
+            assert torch.equal(x.view, y.view)
+
+
+@pytest.mark.parametrize("rows,cols", ODD_SIZES)
+@pytest.mark.parametrize("kind,res,dres,shift,pad", [("f32", "f32", True, 0, 0), ("bf16", "f32", True, 1, 0), ("f16", "f16", False, 3, 5),
+                                                     ("bf16", "bf16", True, 0, 1), ("f16", "f32", False, 1, 3)])
+def test_norm_backward_rows_off_the_boundaries(ap, rows, cols, kind, res, dres, shift, pad):
+    t, rt = TYPES[kind], TYPES[res]
+    dy, h, w, r, d = grad_case(rows, cols, t, rt, dres, seed=rows)
+    bufs = [Strided(rows, cols, t, cols + pad, shift, dy), Strided(rows, cols, rt, cols + pad, shift, h)]
+    more = Strided(rows, cols, rt, cols + 2 * pad, shift + 1, d) if dres else None
+    dx, dw = Strided(rows, cols, rt, cols + pad, 1), torch.empty(cols, device="cuda")
+    ws = torch.empty(ap.ap_rms_norm_backward_workspace(rows, cols), dtype=torch.uint8, device="cuda")
+    ap.ap_rms_norm_backward(bufs[0].view, bufs[1].view, w, r, dx.view, dw, ws, dresidual=more.view if dres else None)
+    done(ap)
+    assert dx.intact() and torch.equal(bufs[0].view, dy) and torch.equal(bufs[1].view, h)
+    check_grad(dx.view, dw, dy, h, w, r, d)
+    ap.ap_rms_norm_backward(bufs[0].view, bufs[1].view, w, r, bufs[1].view, dresidual=more.view if dres else None)  # in place
+    done(ap)
+    assert bufs[1].intact() and torch.equal(bufs[1].view, dx.view)
+
+
+def test_norm_ring_first_and_last_unit(ap):
+    """Rows at the very start and end of what the caller owns, beside NaN: nothing of the neighbours gets in."""
+    rows, cols = 300, 1029
+    flat = torch.full((rows * cols + 16,), float("nan"), dtype=torch.float16, device="cuda")
+    x = flat[3:3 + rows * cols].view(rows, cols)
+    x.copy_(randn(rows, cols).half())
+    w, y, r = torch.ones(cols, device="cuda"), torch.empty(rows, cols, dtype=torch.float16, device="cuda"), torch.empty(rows, device="cuda")
+    ap.ap_debug_set(ap.AP_DBG_FORCE_PATH, 1)
+    ap.ap_rms_norm(x, w, 1e-5, y=y, rstd=r)
+    done(ap)
+    assert ap.ap_debug_get(ap.AP_DBG_LAST_FLAGS) == 12
+    rr = fu.norm(f64(x), None, f64(w), 1e-5)[1]
+    assert np.all(np.abs(f64(r) - rr) <= (fu.DEPTH / 2 + 8) * U * rr) and bool(y.isfinite().all().item())
+
+
 def test_norm_ring_bounded_wait(ap):
     """Rows that never arrive: both ring kernels give up, the error is reported once, and the next calls work."""
     x, w = randn(2000, 512), torch.ones(512, device="cuda")
