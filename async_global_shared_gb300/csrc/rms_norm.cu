@@ -328,7 +328,13 @@ ap_status launch_norm_t(const DeviceInfo& di, const Options& o, const NormArgs& 
     const bool whole =
         a.cols % 8 == 0 && P.vec_x && (!res || P.vec_r) && P.vec_w && (a.y == nullptr || P.vec_y) && (a.q == nullptr || P.vec_q);
     const bool many = o.force_path == 1 || (o.force_path != 2 && a.cols > kRingColumns && a.rows >= kRingElements / a.cols);
-    if (many && plan_ring(di, o, &ring, res ? 2 : 1, in, ld, size, nullptr, a.rows, a.cols, whole)) {
+    // One input alone leaves little to stream beside the work on a row, and a
+    // CTA's one or two wide teams then wait on their sums with nothing else to
+    // do (no residual, y in f16: 9728 x 12000 107 us against 95 in registers,
+    // 9728 x 6000 55 against 49; with two teams of four chunks 9728 x 8192 63
+    // against 71; with a residual 145 against 205 at 9728 x 12000).
+    const auto idle = [&] { return o.force_path != 1 && !res && (ring.teams == 1 || (ring.teams == 2 && ring.chunks == 3)); };
+    if (many && plan_ring(di, o, &ring, res ? 2 : 1, in, ld, size, nullptr, a.rows, a.cols, whole) && !idle()) {
         if (whole)
             return res ? launch_norm_ring<T, R, true, false>(di, P, ring, stream) : launch_norm_ring<T, T, false, false>(di, P, ring, stream);
         return res ? launch_norm_ring<T, R, true, true>(di, P, ring, stream) : launch_norm_ring<T, T, false, true>(di, P, ring, stream);

@@ -259,6 +259,11 @@ __global__ void __launch_bounds__(256) sum_partials_kernel(const float* part, fl
     }
 }
 
+// The ring's set-up is not paid back where a CTA has two rows at most and they
+// are few elements in all (304 x 1000: 11.5 us against 10.6 without, 608 x
+// 1001: 11.8 against 10.6; the other way 1216 x 1001: 11.5 against 14.9, 304 x
+// 11003: 15.6 against 23.5).
+constexpr int64_t kFewElements = int64_t(1) << 20;
 constexpr int64_t kGradSMs = 152;  // the partials' number is part of the interface (workspace size), so no device query
 
 template <typename T, typename R, int C>
@@ -298,7 +303,8 @@ ap_status launch_grad_t(const DeviceInfo& di, const Options& o, const NormGradAr
                        reinterpret_cast<uintptr_t>(a.weight) % 16 == 0;
     if (grid > 0) {
         ap_status st;
-        if (plan_ring(di, o, &ring, res ? 3 : 2, in, ld, size, a.rstd, a.rows, a.cols, whole)) {
+        const bool few = a.rows <= 4 * kGradSMs && a.rows <= kFewElements / a.cols;
+        if (o.force_path != 2 && (o.force_path == 1 || !few) && plan_ring(di, o, &ring, res ? 3 : 2, in, ld, size, a.rstd, a.rows, a.cols, whole)) {
             grid = ring_grid(ring, kGradSMs);
             if (whole)
                 st = res ? launch_grad_ring<T, R, true, false>(di, P, ring, stream) : launch_grad_ring<T, R, false, false>(di, P, ring, stream);

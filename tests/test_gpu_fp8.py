@@ -635,17 +635,33 @@ def test_norm_rows_off_the_boundaries(ap, rows, cols, kind, res, shift, pad):
 def test_norm_backward_rows_off_the_boundaries(ap, rows, cols, kind, res, dres, shift, pad):
     t, rt = TYPES[kind], TYPES[res]
     dy, h, w, r, d = grad_case(rows, cols, t, rt, dres, seed=rows)
-    bufs = [Strided(rows, cols, t, cols + pad, shift, dy), Strided(rows, cols, rt, cols + pad, shift, h)]
-    more = Strided(rows, cols, rt, cols + 2 * pad, shift + 1, d) if dres else None
-    dx, dw = Strided(rows, cols, rt, cols + pad, 1), torch.empty(cols, device="cuda")
+    for path in (1, 2):
+        ap.ap_debug_set(ap.AP_DBG_FORCE_PATH, path)
+        bufs = [Strided(rows, cols, t, cols + pad, shift, dy), Strided(rows, cols, rt, cols + pad, shift, h)]
+        more = Strided(rows, cols, rt, cols + 2 * pad, shift + 1, d) if dres else None
+        at = more.view if dres else None
+        dx, dw = Strided(rows, cols, rt, cols + pad, 1), torch.empty(cols, device="cuda")
+        ws = torch.empty(ap.ap_rms_norm_backward_workspace(rows, cols), dtype=torch.uint8, device="cuda")
+        ap.ap_rms_norm_backward(bufs[0].view, bufs[1].view, w, r, dx.view, dw, ws, dresidual=at)
+        done(ap)
+        assert dx.intact() and torch.equal(bufs[0].view, dy) and torch.equal(bufs[1].view, h)
+        check_grad(dx.view, dw, dy, h, w, r, d)
+        ap.ap_rms_norm_backward(bufs[0].view, bufs[1].view, w, r, bufs[1].view, dresidual=at)  # in place
+        done(ap)
+        assert bufs[1].intact() and torch.equal(bufs[1].view, dx.view)
+
+
+@pytest.mark.parametrize("rows,cols", RING_SIZES)
+@pytest.mark.parametrize("kind,res,dres", [("f32", "f32", True), ("bf16", "f32", True), ("f16", "f16", False)])
+def test_norm_backward_ring_and_registers(ap, rows, cols, kind, res, dres):
+    dy, h, w, r, d = grad_case(rows, cols, TYPES[kind], TYPES[res], dres, seed=cols)
     ws = torch.empty(ap.ap_rms_norm_backward_workspace(rows, cols), dtype=torch.uint8, device="cuda")
-    ap.ap_rms_norm_backward(bufs[0].view, bufs[1].view, w, r, dx.view, dw, ws, dresidual=more.view if dres else None)
-    done(ap)
-    assert dx.intact() and torch.equal(bufs[0].view, dy) and torch.equal(bufs[1].view, h)
-    check_grad(dx.view, dw, dy, h, w, r, d)
-    ap.ap_rms_norm_backward(bufs[0].view, bufs[1].view, w, r, bufs[1].view, dresidual=more.view if dres else None)  # in place
-    done(ap)
-    assert bufs[1].intact() and torch.equal(bufs[1].view, dx.view)
+    for path in (1, 2):
+        ap.ap_debug_set(ap.AP_DBG_FORCE_PATH, path)
+        dx, dw = torch.full_like(h, float("nan")), torch.empty(cols, device="cuda")
+        ap.ap_rms_norm_backward(dy, h, w, r, dx, dw, ws, dresidual=d)
+        done(ap)
+        check_grad(dx, dw, dy, h, w, r, d)
 
 
 def test_norm_ring_first_and_last_unit(ap):
