@@ -5,7 +5,9 @@
 // scale of a block needs its amax before the first code, so a tile of
 // 128 x 128 elements stays in registers between the two; the transposed codes
 // cross through shared memory, where a thread's eight rows of one column are
-// one 8-byte unit.
+// one 8-byte unit. 16384 x 8192 bf16 both ways: 96 us = 5.7 TB/s; a float weight
+// of 11003 x 4100 by tiles, both ways: 47 us = 5.7 TB/s; 64 x 16384 by rows: 6.4
+// us, nearly all of it the call.
 #include "device_common.cuh"
 #include "fp8_common.cuh"
 #include "internal.h"

@@ -2,7 +2,12 @@
 // bits and / or e4m3. For a row of N values:
 //     h = x + residual,  r = 1 / sqrt(sum(h^2) / N + eps),  y = h r w.
 // The sum comes before the first output, so a row is held in registers between
-// the two and memory is passed over once.
+// the two and memory is passed over once. Memory bounds it: 32768 x 8192 bf16
+// with a 32-bit residual, e4m3 out, 432 us = 6.85 TB/s; 16384 x 8192 with a bf16
+// residual 144 us; 1237 x 5000 f16, both outputs, 8.6 us; one row of 4096 2.3 us
+// on the device. Rows off the 16-byte boundaries move element by element, where
+// instructions bound it: 27513 x 3163 f16 with a 32-bit residual 225 us = 4.3
+// TB/s.
 #include "row_ring.cuh"
 
 namespace ap {
@@ -137,7 +142,9 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) rms_norm_kernel(const __gri
 }
 
 // The ring's form: teams of warps, rows from shared memory, the weight in
-// registers for the whole grid's life (four chunks: in shared memory).
+// registers for the whole grid's life (four chunks: in shared memory). One row a
+// CTA leaves the memory idle while the row's sum is on its way: 16384 x 8192
+// took 235 us so, 144 with the ring.
 template <typename T, typename R, int C, bool RES, Weights W, bool SPREAD>
 __global__ void __launch_bounds__(kRingThreads, 1)
     rms_norm_ring_kernel(const __grid_constant__ NormParams P, const __grid_constant__ RowRing ring) {

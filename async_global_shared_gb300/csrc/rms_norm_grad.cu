@@ -2,7 +2,10 @@
 // every h of the row, d r / d h_i = -r^3 h_i / N, so
 //     dx = r (g - n mean(g n)) + dresidual,   dw_j = sum over rows of dy n.
 // The mean comes before the first dx, so a row is held on the chip between the
-// two and memory is passed over once.
+// two and memory is passed over once. Memory bounds it: 16384 x 8192 bf16 with
+// dresidual 161 us = 6.7 TB/s (415 with one row a CTA in registers); 777 x 2560
+// f32 11.6 us, of which 4 are the two kernels' launches; 6062 x 2694 f16 and f32,
+// rows off the 16-byte boundaries, 37 us = 4.4 TB/s.
 #include "row_ring.cuh"
 
 namespace ap {
@@ -12,7 +15,7 @@ struct GradParams {
     NormGradArgs a;
 };
 
-// CTA b takes rows b, b + grid, ...; a thread keeps its columns' share of
+// Few rows, or wider than the ring takes: CTA b takes rows b, b + grid, ...; a thread keeps its columns' share of
 // dweight in registers and writes it to the CTA's row of the workspace at the
 // end, so the sum's order depends on the sizes alone.
 template <typename T, typename R, int C, bool SPREAD>

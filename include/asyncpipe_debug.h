@@ -28,7 +28,9 @@ typedef enum ap_debug_key {
                                    starts on a 16-byte boundary (shift * cols a multiple of 4, and
                                    rows * cols too for a nonzero shift): each stage one 2-D box of
                                    1 KiB lines of the input where it fits, else 1-D boxes of 256
-                                   floats; the 1-D bulk producer otherwise */
+                                   floats; the 1-D bulk producer otherwise. ap_rms_norm and its
+                                   gradient: 1 the ring of rows wherever a row fits it, 2 rows held
+                                   in registers */
     AP_DBG_EXPECT_TX_EXTRA = 2, /* bytes added to every stage's expected transaction count:
                                    the barrier then never completes and the consumers' bounded
                                    waits give up (fault injection; 0 = off) */
@@ -94,7 +96,12 @@ typedef enum ap_debug_key {
                                    or unaligned tail); bit 1: some stage used the scalar
                                    shared-memory path (input/output alignments differ or wrap);
                                    bit 2: the tensor-map producer ran; bit 3: with the line
-                                   view (2-D boxes of whole stages) set up beside the flat map */
+                                   view (2-D boxes of whole stages) set up beside the flat map.
+                                   Norm and gradient: bit 0 a row a warp, bit 1 rows too wide for
+                                   registers, bit 2 the ring, bit 3 rows off the 16-byte
+                                   boundaries. 8-bit product: bit 0 the weight on the
+                                   accumulator's rows, bit 1 pairs of CTAs, bits 4 and up the
+                                   CTAs that share a tile's k */
 } ap_debug_key;
 
 /* Set a settable key. AP_ERR_ARG for an unknown key or a negative value. */
