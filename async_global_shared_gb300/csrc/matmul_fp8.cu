@@ -13,7 +13,7 @@
 //    operand, so a tile's operands cross the L2 once for two SMs; a persistent
 //    grid walks the tiles;
 //  - one CTA a 128 x 128 tile, where there are too few tiles of the former;
-//  - SWAP: few rows of a. The weight b takes the P side, so that its rows fill
+//  - SWAP: at most 32 rows of a. The weight b takes the P side, so that its rows fill
 //    the 128 accumulator rows, and a's rows are the narrow side.
 // The last two split k over the CTAs of a cluster where tiles are few: each
 // sums its share, and the shares are added through distributed shared memory
@@ -90,7 +90,7 @@ struct Form {
     static constexpr int kBuffers = CG == 2 ? 512 / BN : 2;
     static constexpr uint32_t kTmemCols = kBuffers * kRun * BN;
     // CTAs an SM: the narrow forms wait more than they compute
-    static constexpr int kCtas = BN > 64 ? 1 : 2;
+    static constexpr int kCtas = SWAP ? 2 : 1;
     // c leaves through shared memory: a consumer warp's 32 rows of 128 bytes
     static constexpr uint32_t kStagingBytes = SWAP ? 0 : 32 * 128 * kConsumerWarps;
     static constexpr size_t kRingBytes = size_t(STAGES) * kStageBytes;
@@ -681,9 +681,14 @@ ap_status launch_form(const DeviceInfo& di, MatmulParams P, const MatmulArgs& a,
 template <typename C>
 ap_status launch_mm(const DeviceInfo& di, const MatmulParams& P, const MatmulArgs& a, cudaStream_t stream) {
     const bool rows = a.b_block_rows == 1;
+    // Few rows: the weight on the accumulator's rows, a's rows padded to 16 or
+    // 32 (times 8192 x 8192: one row 14.9 us, 15.4 padded to 32; 32 rows 17.0,
+    // 48 in the 128 x 128 form 18.7).
     if (a.m <= 16) return launch_form<C, 16, 1, 5, true, true>(di, P, a, stream);
     if (a.m <= 32) return launch_form<C, 32, 1, 4, true, true>(di, P, a, stream);
-    if (a.m <= 64) return launch_form<C, 64, 1, 4, true, true>(di, P, a, stream);
+    // Pairs from half the SMs' worth of their tiles on (8192^3: 431 us against
+    // 596 one CTA a tile; the other way 333 x 4104 x 5000, 34 pairs: 18.6
+    // against 22.5).
     const int64_t pairs = (a.m + 2 * kTile - 1) / (2 * kTile) * ((a.n + 255) / 256);
     if (pairs >= di.sms / 4)
         return rows ? launch_form<C, 256, 2, 5, true, false>(di, P, a, stream)

@@ -351,6 +351,11 @@ MM_SIZES = [(1, 1, 1), (1, 128, 128), (1, 1000, 4096), (2, 257, 130), (7, 129, 1
             (200, 520, 2100), (333, 1000, 384), (512, 768, 4096), (1000, 2050, 520)]
 
 
+# many blocks of k a CTA in every form: the rings and the scales' slots go round several times
+LONG_SIZES = [(1, 8192, 8192), (12, 20000, 1900), (30, 20000, 1900), (24, 8192, 8192), (48, 8192, 4096), (64, 8192, 8192),
+              (100, 9000, 2600), (600, 5000, 4000)]
+
+
 def operand(rows, cols, tile, seed):
     """Random codes (every finite e4m3 value) and scales."""
     g = torch.Generator().manual_seed(seed)
@@ -376,6 +381,32 @@ def check_matmul(ap, m, n, k, tile, t, c=None, seed=0):
         c[torch.from_numpy(over).cuda()] = 0
     err, near = np.abs(f64(c) - want), fu.matmul_bound(want, terms, k, t)
     assert np.all(err <= near), f"{m}x{n}x{k}: worst {np.nanmax(err / near)} of the bound"
+
+
+@pytest.mark.parametrize("m,n,k", LONG_SIZES)
+@pytest.mark.parametrize("tile", [1, 128])
+def test_matmul_long_runs(ap, m, n, k, tile):
+    for seed in range(2):
+        check_matmul(ap, m, n, k, tile, torch.bfloat16, seed=seed)
+
+
+def test_matmul_calls_one_behind_another(ap):
+    """Calls that start early behind the ones before, through every form: each gives what it gives alone."""
+    cases, alone = [], []
+    for m, n, k in ((1, 4096, 4096), (16, 8192, 2048), (32, 8192, 4096), (64, 4096, 4096), (333, 2000, 2000), (2048, 2048, 2048)):
+        a, sa = operand(m, k, 1, m)
+        b, sb = operand(n, k, 128, n)
+        cases.append((a, sa, b, sb, torch.empty(m, n, device="cuda")))
+    for a, sa, b, sb, c in cases:
+        ap.ap_matmul_fp8(a, sa, b, sb, c)
+        done(ap)
+        alone.append(c.clone())
+        c.fill_(float("nan"))
+    for _ in range(200):
+        for a, sa, b, sb, c in cases:
+            ap.ap_matmul_fp8(a, sa, b, sb, c)
+    done(ap)
+    assert all(torch.equal(case[4], want) for case, want in zip(cases, alone))
 
 
 @pytest.mark.parametrize("m,n,k", MM_SIZES)
