@@ -687,10 +687,12 @@ ap_status launch_mm(const DeviceInfo& di, const MatmulParams& P, const MatmulArg
     if (a.m <= 16) return launch_form<C, 16, 1, 5, true, true>(di, P, a, stream);
     if (a.m <= 32) return launch_form<C, 32, 1, 4, true, true>(di, P, a, stream);
     // Pairs from half the SMs' worth of their tiles on (8192^3: 431 us against
-    // 596 one CTA a tile; the other way 333 x 4104 x 5000, 34 pairs: 18.6
-    // against 22.5).
+    // 596 one CTA a tile; 1024 x 2560 x 4096, 40 pairs: 19.0 against 25.5; the
+    // other way 333 x 4104 x 5000, 34 pairs: 18.6 against 22.5), but not for
+    // rows that one CTA's tile holds (64 x 16384 x 8192: 28.3 us against 33.8 in
+    // pairs).
     const int64_t pairs = (a.m + 2 * kTile - 1) / (2 * kTile) * ((a.n + 255) / 256);
-    if (pairs >= di.sms / 4)
+    if (a.m > kTile && pairs >= di.sms / 4)
         return rows ? launch_form<C, 256, 2, 5, true, false>(di, P, a, stream)
                     : launch_form<C, 256, 2, 5, false, false>(di, P, a, stream);
     return rows ? launch_form<C, 128, 1, 5, true, false>(di, P, a, stream)

@@ -35,6 +35,9 @@
  *    rounded once, to nearest even.
  *  - Results do not depend on timing: no sum is taken in an order that can
  *    change from call to call.
+ *  - Pointers are device memory. A call may be captured into a graph once a
+ *    call of the same sizes, types and alignment has run outside capture (sizes
+ *    choose between kernels, and each has one-time attributes).
  */
 #ifndef ASYNCPIPE_FP8_H
 #define ASYNCPIPE_FP8_H
