@@ -22,12 +22,12 @@
 // What bounds it. One token times 8192 x 8192: the weight's bytes, 14.9 us = 4.5
 // TB/s, of which 5 are the launch, the first loads and the reduction (8 tokens
 // times 28672 x 8192: 39 us = 6.0 TB/s). 128 x 128 tiles: shared memory, 512
-// cycles a block (333 x 4104 x 5000: 18.6 us). 8192^3 in pairs: 431 us = 2.55
-// PFLOP/s, 400 before the power limit lowers the clocks (803 with one CTA a
+// cycles a block (333 x 4104 x 5000: 18.6 us). 8192^3 in pairs: 440 us = 2.5
+// PFLOP/s, 410 before the power limit lowers the clocks (596 with one CTA a
 // 128 x 128 tile): the consumers, whose loads, sums and hand-over of a block
 // take about 850 cycles beside 512 of matrix instructions. Scales by column on
 // top: two operations a value, and the column scales' loads (4096 x 8192 x
-// 16384: 707 us = 1.55 PFLOP/s; 599 without the loads).
+// 16384: 701 us = 1.57 PFLOP/s; 599 without the loads).
 //
 // Roles in a CTA, each a warp: the producer streams the operands' 128-byte
 // wide boxes through a ring of shared-memory stages (tensor maps, 128-byte
@@ -498,7 +498,7 @@ __global__ void __launch_bounds__(Form<BN, CG, STAGES, PER_COL, SWAP>::kThreads,
                             const int rows = static_cast<int>(P.np - row0 < 32 ? P.np - row0 : 32);  // may be negative
                             const int cols = static_cast<int>(P.nq - col0 < kPiece ? P.nq - col0 : kPiece);
                             C* out = static_cast<C*>(P.c) + (row0 * P.ldc + col0);
-#pragma unroll 8
+#pragma unroll 2
                             for (int i = 0; i < rows; ++i, out += P.ldc) {
 #pragma unroll
                                 for (int e = lane; e < kPiece; e += 32) {
@@ -686,7 +686,7 @@ ap_status launch_mm(const DeviceInfo& di, const MatmulParams& P, const MatmulArg
     // 48 in the 128 x 128 form 18.7).
     if (a.m <= 16) return launch_form<C, 16, 1, 5, true, true>(di, P, a, stream);
     if (a.m <= 32) return launch_form<C, 32, 1, 4, true, true>(di, P, a, stream);
-    // Pairs from half the SMs' worth of their tiles on (8192^3: 431 us against
+    // Pairs from half the SMs' worth of their tiles on (8192^3: 440 us against
     // 596 one CTA a tile; 1024 x 2560 x 4096, 40 pairs: 19.0 against 25.5; the
     // other way 333 x 4104 x 5000, 34 pairs: 18.6 against 22.5), but not for
     // rows that one CTA's tile holds (64 x 16384 x 8192: 28.3 us against 33.8 in
