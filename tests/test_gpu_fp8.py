@@ -307,6 +307,24 @@ def test_quantize_strided(ap, tile, shift, pad):
         assert torch.equal(scales.cpu(), ws) and torch.equal(got.view.cpu(), wq.view(torch.uint8))
 
 
+@pytest.mark.parametrize("shift", range(8))
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("out", ["rows", "cols"])
+def test_quantize_rows_at_every_place_of_a_unit(ap, shift, kind, out):
+    rows, cols = 40, 411
+    x = Strided(rows, cols, TYPES[kind], cols + 2 * (shift % 2), shift, randn(rows, cols, seed=shift).to(TYPES[kind]))
+    q, s, qt, st = quant_buffers(rows, cols, 1)
+    v = x.view.float().cpu()
+    if out == "rows":
+        ap.ap_quantize(x.view, 1, q, s)
+    else:
+        ap.ap_quantize(x.view, 1, None, None, qt, st)
+        q, s, v = qt, st, v.t().contiguous()
+    done(ap)
+    wq, ws = fu.codes_32(v, 1)
+    assert torch.equal(s.cpu(), ws) and torch.equal(q.cpu().view(torch.uint8), wq.view(torch.uint8))
+
+
 @pytest.mark.parametrize("tile", [1, 128])
 def test_quantize_extremes(ap, tile):
     """Zeros, subnormals, the largest floats, infinities and NaN, each in a block of its own."""
