@@ -91,6 +91,7 @@ EXPORTED = (
     "ap_debug_fma_probe",
     "ap_debug_fma_probe_horner",
     "ap_debug_scale_pages_async",
+    "ap_debug_norm_grad_ctas",
     "ap_rms_norm",
     "ap_rms_norm_backward",
     "ap_rms_norm_backward_workspace",
@@ -166,6 +167,8 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.ap_rms_norm_backward_workspace.restype = _i64
     lib.ap_quantize.argtypes = [vp, _i64, i32, _i64, _i64, i32, vp, _i64, vp, vp, _i64, vp, vp]
     lib.ap_matmul_fp8.argtypes = [vp, _i64, vp, vp, _i64, vp, i32, vp, _i64, i32, _i64, _i64, _i64, vp]
+    lib.ap_debug_norm_grad_ctas.argtypes = [_i64, _i64, i32, i32, i32, i32]
+    lib.ap_debug_norm_grad_ctas.restype = _i64
     for name in ("ap_rms_norm", "ap_rms_norm_backward", "ap_quantize", "ap_matmul_fp8", "ap_scale", "ap_scale_sync", "ap_row_roll", "ap_poly", "ap_cluster_exchange",
                  "ap_cluster_exchange_ex", "ap_cluster_all_to_all", "ap_masked_copy", "ap_autotune", "ap_autotune_reset", "ap_check",
                  "ap_debug_set", "ap_debug_emulate_ring", "ap_debug_emulate_ring_tensor", "ap_debug_fma_probe",
@@ -344,6 +347,10 @@ def ap_debug_fma_probe_horner(out, out_elems: int, iters: int, stream=None):
 def ap_debug_scale_pages_async(inp, out, n_tiles: int, tile_elems: int, alpha: float, stream=None):
     _check(load().ap_debug_scale_pages_async(_addr(inp), _addr(out), n_tiles, tile_elems, alpha, _stream(stream)),
            "ap_debug_scale_pages_async")
+
+
+def ap_debug_norm_grad_ctas(rows: int, cols: int, type: int, residual_type: int, dresidual: bool, sms: int) -> int:
+    return load().ap_debug_norm_grad_ctas(rows, cols, type, residual_type, int(dresidual), sms)
 
 
 # ------------------------------------------------------------------ 8-bit block-scaled operators

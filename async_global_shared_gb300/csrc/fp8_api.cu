@@ -149,6 +149,23 @@ ap_status ap_rms_norm_backward(const void* dy, int64_t lddy, ap_dtype type, cons
     return launch_rms_norm_backward(di, options(), a, stream);
 }
 
+int64_t ap_debug_norm_grad_ctas(int64_t rows, int64_t cols, int type, int residual_type, int dresidual, int sms) {
+    const ap_dtype t = static_cast<ap_dtype>(type), rt = static_cast<ap_dtype>(residual_type);
+    if (!valid_type(t) || (rt != t && rt != AP_F32) || rows < 0 || cols < 1 || cols > kMaxElems / (rows > 0 ? rows : 1) || sms < 1)
+        return -1;
+    DeviceInfo di{};
+    di.sms = sms;
+    NormGradArgs a{};  // planned, not launched: addresses stand for aligned ones
+    a.rows = rows;
+    a.cols = a.lddy = a.ldh = a.lddr = a.lddx = cols;
+    a.type = t;
+    a.residual_type = rt;
+    a.weight_type = AP_F32;
+    a.rstd = reinterpret_cast<const float*>(256);
+    a.dresidual = dresidual ? a.rstd : nullptr;
+    return norm_grad_ctas(di, options(), a);
+}
+
 ap_status ap_quantize(const void* x, int64_t ldx, ap_dtype type, int64_t rows, int64_t cols, int block_rows, uint8_t* q,
                       int64_t ldq, float* scales, uint8_t* qt, int64_t ldqt, float* scales_t, cudaStream_t stream) {
     if (!valid_type(type) || (block_rows != 1 && block_rows != 128)) return AP_ERR_ARG;

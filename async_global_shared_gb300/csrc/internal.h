@@ -194,8 +194,10 @@ struct NormGradArgs {
 };
 ap_status launch_rms_norm_backward(const DeviceInfo& di, const Options& o, const NormGradArgs& a,
                                    cudaStream_t stream);
-// Rows of partial sums (cols floats each) the launcher above writes at most.
+// Rows of partial sums (cols floats each) the launcher above writes at most,
+// and those it writes and sums for a call.
 int64_t norm_grad_partials(int64_t rows, int64_t cols);
+int64_t norm_grad_ctas(const DeviceInfo& di, const Options& o, const NormGradArgs& a);
 
 struct QuantArgs {
     const void* x;

@@ -299,17 +299,17 @@ ap_status launch_norm_c(const NormParams& P, bool whole, cudaStream_t stream) {
 }
 
 template <typename T, typename R, bool RES, bool SPREAD>
-ap_status launch_norm_ring(const DeviceInfo& di, const NormParams& P, const RowRing& ring, cudaStream_t stream) {
+ap_status launch_norm_ring(const DeviceInfo& di, const NormParams& P, const RowRing& ring, int64_t grid, cudaStream_t stream) {
     static std::atomic<int> configured[5][64];
     if (ring.chunks == 2)
-        return launch_ring_kernel(di, rms_norm_ring_kernel<T, R, 2, RES, IN_REGISTERS, SPREAD>, configured[0], P, ring, PATH_NORM, stream);
+        return launch_ring_kernel(di, rms_norm_ring_kernel<T, R, 2, RES, IN_REGISTERS, SPREAD>, configured[0], P, ring, grid, PATH_NORM, stream);
     if (ring.chunks == 3)
         return ring.keep_weights
-                   ? launch_ring_kernel(di, rms_norm_ring_kernel<T, R, 3, RES, IN_SHARED, SPREAD>, configured[1], P, ring, PATH_NORM, stream)
-                   : launch_ring_kernel(di, rms_norm_ring_kernel<T, R, 3, RES, IN_L2, SPREAD>, configured[2], P, ring, PATH_NORM, stream);
+                   ? launch_ring_kernel(di, rms_norm_ring_kernel<T, R, 3, RES, IN_SHARED, SPREAD>, configured[1], P, ring, grid, PATH_NORM, stream)
+                   : launch_ring_kernel(di, rms_norm_ring_kernel<T, R, 3, RES, IN_L2, SPREAD>, configured[2], P, ring, grid, PATH_NORM, stream);
     return ring.keep_weights
-               ? launch_ring_kernel(di, rms_norm_ring_kernel<T, R, 4, RES, IN_SHARED, SPREAD>, configured[3], P, ring, PATH_NORM, stream)
-               : launch_ring_kernel(di, rms_norm_ring_kernel<T, R, 4, RES, IN_L2, SPREAD>, configured[4], P, ring, PATH_NORM, stream);
+               ? launch_ring_kernel(di, rms_norm_ring_kernel<T, R, 4, RES, IN_SHARED, SPREAD>, configured[3], P, ring, grid, PATH_NORM, stream)
+               : launch_ring_kernel(di, rms_norm_ring_kernel<T, R, 4, RES, IN_L2, SPREAD>, configured[4], P, ring, grid, PATH_NORM, stream);
 }
 
 // The ring's set-up is paid back from this many elements on (1216 x 4096: 8.2
@@ -342,9 +342,12 @@ ap_status launch_norm_t(const DeviceInfo& di, const Options& o, const NormArgs& 
     // against 71; with a residual 145 against 205 at 9728 x 12000).
     const auto idle = [&] { return o.force_path != 1 && !res && (ring.teams == 1 || (ring.teams == 2 && ring.chunks == 3)); };
     if (many && plan_ring(di, o, &ring, res ? 2 : 1, in, ld, size, nullptr, a.rows, a.cols, whole) && !idle()) {
+        const int64_t grid = ring_grid(ring, di.sms, o.grid);
         if (whole)
-            return res ? launch_norm_ring<T, R, true, false>(di, P, ring, stream) : launch_norm_ring<T, T, false, false>(di, P, ring, stream);
-        return res ? launch_norm_ring<T, R, true, true>(di, P, ring, stream) : launch_norm_ring<T, T, false, true>(di, P, ring, stream);
+            return res ? launch_norm_ring<T, R, true, false>(di, P, ring, grid, stream)
+                       : launch_norm_ring<T, T, false, false>(di, P, ring, grid, stream);
+        return res ? launch_norm_ring<T, R, true, true>(di, P, ring, grid, stream)
+                   : launch_norm_ring<T, T, false, true>(di, P, ring, grid, stream);
     }
     if (a.cols <= 256) return launch_norm_c<T, R, 1, true>(P, whole, stream);
     if (a.cols <= 512) return launch_norm_c<T, R, 2, true>(P, whole, stream);

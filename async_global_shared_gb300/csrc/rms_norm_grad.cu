@@ -279,57 +279,85 @@ ap_status run_grad(const GradParams& P, bool whole, int64_t grid, cudaStream_t s
 }
 
 template <typename T, typename R, bool RES, bool SPREAD>
-ap_status launch_grad_ring(const DeviceInfo& di, const GradParams& P, const RowRing& ring, cudaStream_t stream) {
+ap_status launch_grad_ring(const DeviceInfo& di, const GradParams& P, const RowRing& ring, int64_t grid, cudaStream_t stream) {
     static std::atomic<int> configured[5][64];
     if (ring.chunks == 2)
-        return launch_ring_kernel(di, rms_norm_grad_ring_kernel<T, R, 2, RES, IN_REGISTERS, SPREAD>, configured[0], P, ring, PATH_NORM_GRAD, stream);
+        return launch_ring_kernel(di, rms_norm_grad_ring_kernel<T, R, 2, RES, IN_REGISTERS, SPREAD>, configured[0], P, ring, grid, PATH_NORM_GRAD, stream);
     if (ring.chunks == 3)
         return ring.keep_weights
-                   ? launch_ring_kernel(di, rms_norm_grad_ring_kernel<T, R, 3, RES, IN_SHARED, SPREAD>, configured[1], P, ring, PATH_NORM_GRAD, stream)
-                   : launch_ring_kernel(di, rms_norm_grad_ring_kernel<T, R, 3, RES, IN_L2, SPREAD>, configured[2], P, ring, PATH_NORM_GRAD, stream);
+                   ? launch_ring_kernel(di, rms_norm_grad_ring_kernel<T, R, 3, RES, IN_SHARED, SPREAD>, configured[1], P, ring, grid, PATH_NORM_GRAD, stream)
+                   : launch_ring_kernel(di, rms_norm_grad_ring_kernel<T, R, 3, RES, IN_L2, SPREAD>, configured[2], P, ring, grid, PATH_NORM_GRAD, stream);
     return ring.keep_weights
-               ? launch_ring_kernel(di, rms_norm_grad_ring_kernel<T, R, 4, RES, IN_SHARED, SPREAD>, configured[3], P, ring, PATH_NORM_GRAD, stream)
-               : launch_ring_kernel(di, rms_norm_grad_ring_kernel<T, R, 4, RES, IN_L2, SPREAD>, configured[4], P, ring, PATH_NORM_GRAD, stream);
+               ? launch_ring_kernel(di, rms_norm_grad_ring_kernel<T, R, 4, RES, IN_SHARED, SPREAD>, configured[3], P, ring, grid, PATH_NORM_GRAD, stream)
+               : launch_ring_kernel(di, rms_norm_grad_ring_kernel<T, R, 4, RES, IN_L2, SPREAD>, configured[4], P, ring, grid, PATH_NORM_GRAD, stream);
+}
+
+// Which kernel a call takes, and its CTAs: each writes one row of partial sums,
+// so the sum over them takes the same number.
+struct GradPlan {
+    bool whole, rings;
+    RowRing ring;
+    int64_t grid;
+};
+
+template <typename T, typename R>
+GradPlan plan_grad(const DeviceInfo& di, const Options& o, const NormGradArgs& a) {
+    GradPlan g{};
+    const void* const in[] = {a.dy, a.h, a.dresidual};
+    const int64_t ld[] = {a.lddy, a.ldh, a.lddr}, size[] = {sizeof(T), sizeof(R), sizeof(R)};
+    const bool res = a.dresidual != nullptr;
+    g.whole = a.cols % 8 == 0 && rows_aligned(a.dy, a.lddy, sizeof(T), 16) && rows_aligned(a.h, a.ldh, sizeof(R), 16) &&
+              (!res || rows_aligned(a.dresidual, a.lddr, sizeof(R), 16)) && rows_aligned(a.dx, a.lddx, sizeof(R), 16) &&
+              reinterpret_cast<uintptr_t>(a.weight) % 16 == 0;
+    g.grid = norm_grad_partials(a.rows, a.cols);
+    const bool few = a.rows <= 4 * kGradSMs && a.rows <= kFewElements / a.cols;
+    g.rings = a.rows > 0 && o.force_path != 2 && (o.force_path == 1 || !few) &&
+              plan_ring(di, o, &g.ring, res ? 3 : 2, in, ld, size, a.rstd, a.rows, a.cols, g.whole);
+    if (g.rings) g.grid = std::min(g.grid, ring_grid(g.ring, di.sms, o.grid));
+    return g;
 }
 
 template <typename T, typename R>
 ap_status launch_grad_t(const DeviceInfo& di, const Options& o, const NormGradArgs& a, cudaStream_t stream) {
     GradParams P;
     P.a = a;
-    int64_t grid = norm_grad_partials(a.rows, a.cols);
-    RowRing ring;
-    const void* const in[] = {a.dy, a.h, a.dresidual};
-    const int64_t ld[] = {a.lddy, a.ldh, a.lddr}, size[] = {sizeof(T), sizeof(R), sizeof(R)};
+    const GradPlan g = plan_grad<T, R>(di, o, a);
     const bool res = a.dresidual != nullptr;
-    const bool whole = a.cols % 8 == 0 && rows_aligned(a.dy, a.lddy, sizeof(T), 16) && rows_aligned(a.h, a.ldh, sizeof(R), 16) &&
-                       (!res || rows_aligned(a.dresidual, a.lddr, sizeof(R), 16)) && rows_aligned(a.dx, a.lddx, sizeof(R), 16) &&
-                       reinterpret_cast<uintptr_t>(a.weight) % 16 == 0;
-    if (grid > 0) {
+    if (g.grid > 0) {
         ap_status st;
-        const bool few = a.rows <= 4 * kGradSMs && a.rows <= kFewElements / a.cols;
-        if (o.force_path != 2 && (o.force_path == 1 || !few) && plan_ring(di, o, &ring, res ? 3 : 2, in, ld, size, a.rstd, a.rows, a.cols, whole)) {
-            grid = ring_grid(ring, kGradSMs);
-            if (whole)
-                st = res ? launch_grad_ring<T, R, true, false>(di, P, ring, stream) : launch_grad_ring<T, R, false, false>(di, P, ring, stream);
+        if (g.rings) {
+            if (g.whole)
+                st = res ? launch_grad_ring<T, R, true, false>(di, P, g.ring, g.grid, stream)
+                         : launch_grad_ring<T, R, false, false>(di, P, g.ring, g.grid, stream);
             else
-                st = res ? launch_grad_ring<T, R, true, true>(di, P, ring, stream) : launch_grad_ring<T, R, false, true>(di, P, ring, stream);
+                st = res ? launch_grad_ring<T, R, true, true>(di, P, g.ring, g.grid, stream)
+                         : launch_grad_ring<T, R, false, true>(di, P, g.ring, g.grid, stream);
+        } else if (a.cols <= 4096) {
+            st = run_grad<T, R, 1>(P, g.whole, g.grid, stream);
+        } else if (a.cols <= 8192) {
+            st = run_grad<T, R, 2>(P, g.whole, g.grid, stream);
+        } else if (a.cols <= 16384) {
+            st = run_grad<T, R, 4>(P, g.whole, g.grid, stream);
         } else {
-            if (a.cols <= 4096) {
-                st = run_grad<T, R, 1>(P, whole, grid, stream);
-            } else if (a.cols <= 8192) {
-                st = run_grad<T, R, 2>(P, whole, grid, stream);
-            } else if (a.cols <= 16384) {
-                st = run_grad<T, R, 4>(P, whole, grid, stream);
-            } else {
-                record_launch(PATH_NORM_GRAD, grid, 0, 0, 0, 2);
-                st = launch_early(rms_norm_grad_wide_kernel<T, R>, grid, 1024, stream, P);
-            }
+            record_launch(PATH_NORM_GRAD, g.grid, 0, 0, 0, 2);
+            st = launch_early(rms_norm_grad_wide_kernel<T, R>, g.grid, 1024, stream, P);
         }
         if (st != AP_OK) return st;
     }
     if (a.dweight == nullptr) return AP_OK;
     return launch_early(sum_partials_kernel, (a.cols + 31) / 32, 256, stream, static_cast<const float*>(a.workspace),
-                        a.dweight, grid, a.cols);
+                        a.dweight, g.grid, a.cols);
+}
+
+// f of the kernels' element types for these of the arguments.
+template <typename F>
+auto with_types(const NormGradArgs& a, F f) {
+    const bool same = a.residual_type == a.type;
+    switch (a.type) {
+        case AP_BF16: return same ? f(__nv_bfloat16(), __nv_bfloat16()) : f(__nv_bfloat16(), 0.0f);
+        case AP_F16: return same ? f(__half(), __half()) : f(__half(), 0.0f);
+        default: return f(0.0f, 0.0f);
+    }
 }
 
 }  // namespace
@@ -339,14 +367,11 @@ ap_status launch_grad_t(const DeviceInfo& di, const Options& o, const NormGradAr
 int64_t norm_grad_partials(int64_t rows, int64_t) { return std::min(rows, kGradSMs * 2); }
 
 ap_status launch_rms_norm_backward(const DeviceInfo& di, const Options& o, const NormGradArgs& a, cudaStream_t stream) {
-    const bool same = a.residual_type == a.type;
-    switch (a.type) {
-        case AP_BF16:
-            return same ? launch_grad_t<__nv_bfloat16, __nv_bfloat16>(di, o, a, stream)
-                        : launch_grad_t<__nv_bfloat16, float>(di, o, a, stream);
-        case AP_F16: return same ? launch_grad_t<__half, __half>(di, o, a, stream) : launch_grad_t<__half, float>(di, o, a, stream);
-        default: return launch_grad_t<float, float>(di, o, a, stream);
-    }
+    return with_types(a, [&](auto t, auto r) { return launch_grad_t<decltype(t), decltype(r)>(di, o, a, stream); });
+}
+
+int64_t norm_grad_ctas(const DeviceInfo& di, const Options& o, const NormGradArgs& a) {
+    return with_types(a, [&](auto t, auto r) { return plan_grad<decltype(t), decltype(r)>(di, o, a).grid; });
 }
 
 }  // namespace ap

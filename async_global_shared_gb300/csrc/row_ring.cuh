@@ -311,9 +311,12 @@ bool plan_ring(const DeviceInfo& di, const Options& o, RowRing* R, int inputs, c
     return false;
 }
 
-int64_t ring_grid(const RowRing& R, int64_t sms) {
+// CTAs of a ring kernel: one an SM, each with at least one stage of rows, and
+// no more than the caller's cap (0: none).
+int64_t ring_grid(const RowRing& R, int64_t sms, int64_t cap) {
     const int64_t step = R.together * R.turns;
-    return std::min(sms, (R.rows + step - 1) / step);
+    const int64_t grid = std::min(sms, (R.rows + step - 1) / step);
+    return cap > 0 ? std::min(grid, cap) : grid;
 }
 
 // The weight in floats, by the 16 consumer warps.
@@ -339,10 +342,10 @@ __device__ __forceinline__ void again_weight(const Params& P, const float* kept,
 
 constexpr int64_t kMaxGrid = int64_t(1) << 31;
 
-// Launch of a persistent ring kernel with its shared memory.
+// Launch of a persistent ring kernel of `grid` CTAs with its shared memory.
 template <typename K, typename Params>
 ap_status launch_ring_kernel(const DeviceInfo& di, K kernel, std::atomic<int> (&configured)[64], const Params& P,
-                             const RowRing& ring, int64_t path, cudaStream_t stream) {
+                             const RowRing& ring, int64_t grid, int64_t path, cudaStream_t stream) {
     if (di.device < 0 || di.device >= 64) return AP_ERR_CUDA;
     if (!configured[di.device].load()) {  // attribute set on this device (setting twice is harmless)
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kRingBytes)) !=
@@ -350,7 +353,6 @@ ap_status launch_ring_kernel(const DeviceInfo& di, K kernel, std::atomic<int> (&
             return AP_ERR_CUDA;
         configured[di.device] = 1;
     }
-    const int64_t grid = ring_grid(ring, di.sms);
     const size_t smem = ring.smem;
     record_launch(path, grid, ring.together * ring.turns, static_cast<int64_t>(smem), ring.stages, 4 | (ring.spread ? 8 : 0));
     cudaLaunchConfig_t cfg{};

@@ -37,7 +37,8 @@ typedef enum ap_debug_key {
     AP_DBG_TIMEOUT_NS = 3,      /* limit of every kernel wait in ns (0 = default 2 s, or the
                                    AP_WAIT_TIMEOUT_NS environment variable) */
     AP_DBG_STAGE_BYTES = 4,     /* ring stage payload in bytes (0 = automatic) */
-    AP_DBG_GRID = 5,            /* cap on the number of CTAs of ring kernels (0 = automatic) */
+    AP_DBG_GRID = 5,            /* cap on the number of CTAs of ring kernels, the norm's and its
+                                   gradient's among them (0 = automatic) */
     AP_DBG_CTAS_PER_SM = 6,     /* resident ring CTAs per SM the grid is sized for (0 = 1) */
     AP_DBG_ROLL_STAGES = 7,     /* ring depth used by ap_row_roll (0 = 2) */
     AP_DBG_CONSUMER_WARPS = 8,  /* consumer warps per ring CTA: 8, 12 or 16 (0 = automatic) */
@@ -178,6 +179,15 @@ ap_status ap_debug_emulate_ring(const float* in_host, float* out_host, int64_t n
  */
 ap_status ap_debug_emulate_ring_tensor(const float* in_host, float* out_host, int64_t rows, int64_t cols,
                                        int64_t shift, int64_t line_boxes, int64_t stage_elems);
+
+/*
+ * CTAs ap_rms_norm_backward's first kernel would have on a device of `sms`
+ * SMs, for matrices of these ap_dtypes without gaps at aligned addresses, with
+ * or without dresidual: the rows of the workspace it writes, and those its
+ * second kernel adds up. -1 for sizes or types that are not valid. Makes no
+ * CUDA call.
+ */
+int64_t ap_debug_norm_grad_ctas(int64_t rows, int64_t cols, int type, int residual_type, int dresidual, int sms);
 
 #ifdef __cplusplus
 }
