@@ -58,6 +58,7 @@ AP_DBG_EXCHANGE_BATCH = 16
 AP_DBG_EXCHANGE_SEND_SLOTS = 17
 AP_DBG_RING_RUN = 18
 AP_DBG_CONSUMER_GROUPS = 19
+AP_DBG_GIVE_UP = 20
 AP_DBG_LAST_PATH = 100
 AP_DBG_LAST_GRID = 101
 AP_DBG_LAST_STAGE_ELEMS = 102

@@ -39,6 +39,7 @@ std::atomic<int64_t> g_ex_batch{0};
 std::atomic<int64_t> g_ex_send_slots{0};
 std::atomic<int64_t> g_ring_run{0};
 std::atomic<int64_t> g_consumer_groups{0};
+std::atomic<int64_t> g_give_up{0};
 
 std::atomic<int64_t> g_last_path{0}, g_last_grid{0}, g_last_stage_elems{0}, g_last_smem{0}, g_last_stages{0},
     g_last_flags{0}, g_last_site{0}, g_last_run{0}, g_last_warps{0}, g_last_groups{0}, g_last_chains{0};
@@ -166,6 +167,7 @@ Options options() {
     o.ex_send_slots = g_ex_send_slots.load();
     o.ring_run = g_ring_run.load();
     o.consumer_groups = g_consumer_groups.load();
+    o.give_up = g_give_up.load();
     return o;
 }
 
@@ -497,6 +499,10 @@ ap_status ap_debug_set(int key, int64_t value) {
             if (value > 3) return AP_ERR_ARG;
             g_consumer_groups = value;
             return AP_OK;
+        case AP_DBG_GIVE_UP:
+            if (value > 16) return AP_ERR_ARG;
+            g_give_up = value;
+            return AP_OK;
         default: return AP_ERR_ARG;
     }
 }
@@ -521,6 +527,7 @@ int64_t ap_debug_get(int key) {
         case AP_DBG_EXCHANGE_SEND_SLOTS: return o.ex_send_slots;
         case AP_DBG_RING_RUN: return o.ring_run;
         case AP_DBG_CONSUMER_GROUPS: return o.consumer_groups;
+        case AP_DBG_GIVE_UP: return o.give_up;
         case AP_DBG_LAST_PATH: return g_last_path.load();
         case AP_DBG_LAST_GRID: return g_last_grid.load();
         case AP_DBG_LAST_STAGE_ELEMS: return g_last_stage_elems.load();

@@ -46,6 +46,7 @@ struct Options {
     int64_t ex_send_slots;
     int64_t ring_run;
     int64_t consumer_groups;
+    int64_t give_up;
 };
 
 Options options();

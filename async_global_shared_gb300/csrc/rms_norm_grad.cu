@@ -122,9 +122,10 @@ __global__ void __launch_bounds__(kRingThreads, 1)
     while (s >= ring.stages) s -= ring.stages, ++round;
     for (int64_t base = (blockIdx.x + static_cast<int64_t>(gridDim.x) * group) * step; base < a.rows;
          base += gridDim.x * groups * step) {
-        bool ok = true;
-        if (lane == 0) ok = ring_wait(ring, bars, &bars.full[s], round & 1, SITE_ROWS_CONSUMER);
-        if (!__shfl_sync(0xffffffffu, static_cast<int>(ok), 0)) break;
+        if (!stage_arrived(ring, bars, s, round)) {
+            attend_sums(ring, scratch, team, base + mate, gridDim.x * groups * step, turn);
+            break;
+        }
         const unsigned char* stage = smem + s * ring.stage_bytes;
         for (int m = 0; m < ring.turns; ++m, turn ^= 1) {
             const int slot = m * ring.together + mate;

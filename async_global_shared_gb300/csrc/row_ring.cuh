@@ -108,6 +108,7 @@ struct RowRing {
     int inputs, chunks, team_warps, teams, together, turns, stages;
     int64_t rows;
     uint32_t tx_extra;  // fault injection: bytes every stage waits for in vain
+    int give_up;        // fault injection: the consumer warp, from 1, whose first wait gives up
     uint64_t timeout_ns;
     uint32_t* status;
 };
@@ -136,6 +137,16 @@ __device__ __forceinline__ bool ring_wait(const RowRing& R, RingBars& b, uint64_
     const int w = wait_phase<false>(ptx::smem_addr(bar), parity, R.timeout_ns, &b.abort);
     if (w == WAIT_TIMEOUT) raise_timeout(R.status, site, &b.abort);
     return w == WAIT_OK;
+}
+
+// A consumer warp's wait for stage s, one lane asking.
+__device__ __forceinline__ bool stage_arrived(const RowRing& R, RingBars& b, int s, uint32_t round) {
+    bool ok = true;
+    if ((threadIdx.x & 31) == 0) {
+        ok = R.give_up != static_cast<int>(threadIdx.x >> 5) + 1 && ring_wait(R, b, &b.full[s], round & 1, SITE_ROWS_CONSUMER);
+        if (!ok) raise_timeout(R.status, SITE_ROWS_CONSUMER, &b.abort);
+    }
+    return __shfl_sync(0xffffffffu, static_cast<int>(ok), 0) != 0;
 }
 
 // Where a stage's row `slot` of input i lies in the input's part of the stage
@@ -240,6 +251,20 @@ __device__ __forceinline__ float team_sum(float v, float* scratch, int team, int
     return warp_sum(v);
 }
 
+// For a warp that gave up its wait for the stage whose first row of the team
+// is `row`. Its team mates may have had their answer a moment before or after
+// and count on it at the team's barriers, so it stays for the sums of all the
+// rows that are left to them, stages `apart` rows apart; its part is NaN, and
+// so is what they make of such a row.
+__device__ __forceinline__ void attend_sums(const RowRing& R, float (*scratch)[kRingWarps], int team, int64_t row, int64_t apart,
+                                            int turn) {
+    if (R.team_warps == 1) return;
+    for (; row < R.rows; row += apart)  // (the last stage's turns past the end have no sum)
+        for (int m = 0; m < R.turns; ++m, turn ^= 1)
+            if (row + m * R.together < R.rows)
+                team_sum(__int_as_float(0x7fc00000), &scratch[turn][team * R.team_warps], team, R.team_warps);
+}
+
 // Fill in the plan for rows of `cols` elements; false where the ring does not
 // take these rows (width). whole: the inputs' rows start on 16-byte boundaries
 // and hold a multiple of eight columns.
@@ -249,6 +274,7 @@ bool plan_ring(const DeviceInfo& di, const Options& o, RowRing* R, int inputs, c
     R->spread = !whole;
     R->side = side;
     R->tx_extra = static_cast<uint32_t>(o.tx_extra);
+    R->give_up = static_cast<int>(o.give_up);
     R->timeout_ns = static_cast<uint64_t>(o.timeout_ns);
     R->status = di.status;
     R->inputs = inputs;

@@ -87,6 +87,9 @@ typedef enum ap_debug_key {
                                    stages g, g + groups, ...): 0 automatic, or 1, 2, 3 where the count
                                    divides the consumer warps (16: 1 or 2; 12: 1, 2 or 3; 8: 1) and the
                                    ring depth; other counts make ap_poly return AP_ERR_ARG */
+    AP_DBG_GIVE_UP = 20,        /* ap_rms_norm and its gradient, ring of rows: consumer warp 1..16 of
+                                   every CTA gives up its first wait as if its limit had run out,
+                                   while the others go on (fault injection; 0 = off) */
     AP_DBG_LAST_SITE = 106,     /* where the error ap_check last reported was raised (kernel site code) */
     AP_DBG_LAST_RUN = 107,      /* ring: consecutive stages per CTA, 0 for the persistent grid */
     AP_DBG_LAST_WARPS = 108,    /* ring: consumer warps per CTA */

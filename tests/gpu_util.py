@@ -47,6 +47,7 @@ def reset_debug(ap):
         ap.AP_DBG_EXCHANGE_BATCH,
         ap.AP_DBG_RING_RUN,
         ap.AP_DBG_CONSUMER_GROUPS,
+        ap.AP_DBG_GIVE_UP,
     ):
         ap.ap_debug_set(key, 0)
 

@@ -46,3 +46,11 @@ def test_norm_backward_plan_under_the_cap(ap):
         assert ap.ap_debug_norm_grad_ctas(8192, 4096, ap.AP_BF16, ap.AP_BF16, True, 152) == 20
     finally:
         ap.ap_debug_set(ap.AP_DBG_GRID, 0)
+
+
+def test_give_up_setting(ap):
+    lib = ap.load()
+    assert lib.ap_debug_set(ap.AP_DBG_GIVE_UP, 17) == ap.AP_ERR_ARG and lib.ap_debug_set(ap.AP_DBG_GIVE_UP, -1) == ap.AP_ERR_ARG
+    for value in (16, 0):
+        ap.ap_debug_set(ap.AP_DBG_GIVE_UP, value)
+        assert ap.ap_debug_get(ap.AP_DBG_GIVE_UP) == value
