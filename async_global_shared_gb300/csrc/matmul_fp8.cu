@@ -569,6 +569,7 @@ __global__ void __launch_bounds__(Form<BN, CG, STAGES, PER_COL, SWAP>::kThreads,
                 }
             }
         }
+        __syncwarp();         // lanes' loops above differ in length, and the barrier takes whole warps
         ptx::cluster_sync();  // every share has been read
     }
 }
