@@ -5,7 +5,11 @@
 // stay in the tensor core's accumulator: each block's products go to an
 // accumulator of their own in tensor memory, and consumer threads read it,
 // multiply it by the two scales and add it to sums in registers while the
-// tensor core works on the next blocks.
+// tensor core works on the next blocks. sa sb is one factor, which has to be a
+// float by itself. Orders that keep scales past 2^64 or below 2^-63 in range
+// take another operation a value, and looking for such scales alone costs the
+// consumers 4 to 13 % (8192^3 412 us, 449 with a second loop for blocks that
+// have them; 4096 x 8192 x 16384 702 and 775).
 //
 // Below, P is the operand whose rows are the accumulator's rows (128 a CTA)
 // and Q the one whose rows are its columns (BN a tile). Three forms:

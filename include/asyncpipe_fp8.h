@@ -125,12 +125,17 @@ ap_status ap_quantize(const void* x, int64_t ldx, ap_dtype type, int64_t rows, i
 
 /*
  * ap_matmul_fp8: c = a * b^T of block-scaled 8-bit matrices,
- *     c[i, j] = sum_k (a[i, k] a_scales[i, k / 128]) * (b[j, k] sb),
- * sb = b_scales[j / 128, k / 128] (b_block_rows = 128: b in tiles) or
- * b_scales[j, k / 128] (b_block_rows = 1: b in row blocks).
+ *     c[i, j] = sum over blocks kb of (sa sb) * sum over the block's k of a[i, k] b[j, k],
+ * sa = a_scales[i, kb], sb = b_scales[j / 128, kb] (b_block_rows = 128: b in
+ * tiles) or b_scales[j, kb] (b_block_rows = 1: b in row blocks).
  * The products of a block of 128 are summed by the tensor cores into 32-bit
- * accumulators; each block's sum times its two scales is added to a 32-bit
- * sum.
+ * accumulators; each block's sum times sa sb is added to a 32-bit sum.
+ * The product sa sb is formed first, in 32 bits rounded to nearest, and is to
+ * be a float: past the largest one (two scales of 2^64 and more) it is an
+ * infinity and the term infinite, or NaN where the block's sum is 0; below 2^-126
+ * (two of 2^-63 and less) it is subnormal and has lost bits, and so has the term.
+ * Blocks whose largest magnitudes lie between 2^-54 and 2^72, or are 0, meet
+ * without either.
  *  a            m x k, leading dimension lda; a_scales by row blocks.
  *  b            n x k, leading dimension ldb; b_scales as b_block_rows says.
  *  c            m x n of c_type, leading dimension ldc.
