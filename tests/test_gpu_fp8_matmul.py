@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import fp8_util as fu
-from fp8_util import f64
+from fp8_util import TYPES, Strided, f64
 from gpu_util import device, lib, reset_debug
 from test_gpu_fp8 import check_matmul, done, operand
 
@@ -104,3 +104,88 @@ def test_scales_whose_product_is_no_float(ap, m, n, k, tile):
     ap.ap_matmul_fp8(a, sa, b, sb, c, tile)
     done(ap)
     assert torch.isnan(c[1]).all() and torch.isfinite(c[2:]).all() and torch.isfinite(c[0]).all()
+
+
+# ------------------------------------------------------------------ pairs of CTAs
+#
+# More than 128 rows and at least 38 tiles of 256 x 256. A pair whose second CTA has no rows at all, tiles that end
+# everywhere, k of one block and of many, more tiles than pairs.
+PAIRS = [(129, 9800, 1000), (300, 5000, 384), (1100, 2400, 520), (2048, 2048, 128), (700, 3300, 2600), (2500, 5200, 300), (257, 4900, 1)]
+
+
+@pytest.mark.parametrize("m,n,k", PAIRS)
+@pytest.mark.parametrize("tile", [1, 128])
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+def test_pairs(ap, m, n, k, tile, kind):
+    check_matmul(ap, m, n, k, tile, TYPES[kind], seed=m + k)
+    assert flags(ap) & 3 == 2
+
+
+@pytest.mark.parametrize("m,n,k", [(1100, 2400, 520), (300, 5001, 384), (2500, 5203, 300)])
+@pytest.mark.parametrize("tile", [1, 128])
+@pytest.mark.parametrize("shift,pad", [(0, 8), (1, 3), (8, 24)])
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+def test_pairs_strided_output_stays_inside(ap, m, n, k, tile, shift, pad, kind):
+    """Rows of c on and off the 16-byte boundaries, with guards between and around them."""
+    c = Strided(m, n, TYPES[kind], n + pad, shift)
+    check_matmul(ap, m, n, k, tile, TYPES[kind], c=c.view)
+    assert c.intact() and flags(ap) & 3 == 2
+
+
+@pytest.mark.parametrize("tile", [1, 128])
+def test_pairs_nan_stays_in_its_row_and_column(ap, tile):
+    m, n, k = 1100, 2400, 700
+    a, sa = operand(m, k, 1, 1)
+    b, sb = operand(n, k, tile, 2)
+    rows, cols = [1, 127, 128, 300, 1099], [7, 300, 2399]
+    for r in rows:  # either CTA of a pair, the last rows
+        a.view(torch.uint8)[r, 600] = 0x7F
+    if tile == 1:
+        for j in cols:
+            sb[j, 2] = float("inf")
+    c = torch.empty(m, n, device="cuda")
+    ap.ap_matmul_fp8(a, sa, b, sb, c, tile)
+    done(ap)
+    bad = ~torch.isfinite(c)
+    assert flags(ap) & 3 == 2 and torch.isnan(c[rows]).all()
+    bad[rows] = False
+    if tile == 1:
+        assert not torch.isfinite(c[:, cols]).any()
+        bad[:, cols] = False
+    assert not bad.any()
+
+
+@pytest.mark.parametrize("tile", [1, 128])
+def test_pairs_read_only_k_columns(ap, tile):
+    m, n, k = 1100, 2400, 200
+    a, sa = operand(m, k, 1, 1)
+    b, sb = operand(n, k, tile, 2)
+    wide_a = torch.full((m, 512), 0x7F, dtype=torch.uint8, device="cuda")
+    wide_b = torch.full((n, 512), 0x7F, dtype=torch.uint8, device="cuda")
+    wide_a[:, 16:16 + k].copy_(a.view(torch.uint8))
+    wide_b[:, 32:32 + k].copy_(b.view(torch.uint8))
+    c = [torch.empty(m, n, device="cuda") for _ in range(4)]
+    for out in c[1:]:
+        ap.ap_matmul_fp8(wide_a[:, 16:16 + k], sa, wide_b[:, 32:32 + k], sb, out, tile)
+    ap.ap_matmul_fp8(a, sa, b, sb, c[0], tile)
+    done(ap)
+    assert flags(ap) & 3 == 2 and all(torch.equal(c[0], out) for out in c[1:])
+
+
+@pytest.mark.parametrize("tile", [1, 128])
+def test_pairs_bounded_wait(ap, tile):
+    """A stage that never fills: both CTAs' waits give up, the error is reported once, and the next call works."""
+    m, n, k = 1100, 2400, 1000
+    a, sa = operand(m, k, 1, 1)
+    b, sb = operand(n, k, tile, 2)
+    c = torch.empty(m, n, device="cuda")
+    ap.ap_matmul_fp8(a, sa, b, sb, c, tile)
+    done(ap)
+    assert flags(ap) & 3 == 2
+    ap.ap_debug_set(ap.AP_DBG_TIMEOUT_NS, 2_000_000)
+    ap.ap_debug_set(ap.AP_DBG_EXPECT_TX_EXTRA, 16)
+    ap.ap_matmul_fp8(a, sa, b, sb, c, tile)
+    assert ap.ap_check() == ap.AP_ERR_DEVICE_TIMEOUT
+    assert ap.ap_check() == ap.AP_OK
+    reset_debug(ap)
+    check_matmul(ap, m, n, k, tile, torch.float32)
