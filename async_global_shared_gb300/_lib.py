@@ -93,6 +93,7 @@ EXPORTED = (
     "ap_debug_fma_probe_horner",
     "ap_debug_scale_pages_async",
     "ap_debug_norm_grad_ctas",
+    "ap_debug_block_scale",
     "ap_rms_norm",
     "ap_rms_norm_backward",
     "ap_rms_norm_backward_workspace",
@@ -170,10 +171,11 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.ap_matmul_fp8.argtypes = [vp, _i64, vp, vp, _i64, vp, i32, vp, _i64, i32, _i64, _i64, _i64, vp]
     lib.ap_debug_norm_grad_ctas.argtypes = [_i64, _i64, i32, i32, i32, i32]
     lib.ap_debug_norm_grad_ctas.restype = _i64
+    lib.ap_debug_block_scale.argtypes = [vp, vp, vp, _i64, vp]
     for name in ("ap_rms_norm", "ap_rms_norm_backward", "ap_quantize", "ap_matmul_fp8", "ap_scale", "ap_scale_sync", "ap_row_roll", "ap_poly", "ap_cluster_exchange",
                  "ap_cluster_exchange_ex", "ap_cluster_all_to_all", "ap_masked_copy", "ap_autotune", "ap_autotune_reset", "ap_check",
                  "ap_debug_set", "ap_debug_emulate_ring", "ap_debug_emulate_ring_tensor", "ap_debug_fma_probe",
-                 "ap_debug_fma_probe_horner", "ap_debug_scale_pages_async"):
+                 "ap_debug_fma_probe_horner", "ap_debug_scale_pages_async", "ap_debug_block_scale"):
         getattr(lib, name).restype = ctypes.c_int
     if path is None:
         _lib = lib
@@ -352,6 +354,10 @@ def ap_debug_scale_pages_async(inp, out, n_tiles: int, tile_elems: int, alpha: f
 
 def ap_debug_norm_grad_ctas(rows: int, cols: int, type: int, residual_type: int, dresidual: bool, sms: int) -> int:
     return load().ap_debug_norm_grad_ctas(rows, cols, type, residual_type, int(dresidual), sms)
+
+
+def ap_debug_block_scale(amax, scale, inv, n: int, stream=None):
+    _check(load().ap_debug_block_scale(_addr(amax), _addr(scale), _addr(inv), n, _stream(stream)), "ap_debug_block_scale")
 
 
 # ------------------------------------------------------------------ 8-bit block-scaled operators

@@ -195,6 +195,22 @@ ap_status ap_quantize(const void* x, int64_t ldx, ap_dtype type, int64_t rows, i
     return launch_quantize(di, a, stream);
 }
 
+ap_status ap_debug_block_scale(const float* amax, float* scale, float* inv, int64_t n, cudaStream_t stream) {
+    if (n < 0 || n > (int64_t(1) << 30)) return AP_ERR_SHAPE;
+    if (n == 0) return AP_OK;
+    if (amax == nullptr || scale == nullptr || inv == nullptr) return AP_ERR_NULL;
+    const Matrix all[] = {floats(amax, 1, n), floats(scale, 1, n), floats(inv, 1, n)};
+    for (int i = 0; i < 3; ++i) {
+        if (!aligned(all[i])) return AP_ERR_ALIGN;
+        for (int j = 0; j < i; ++j)
+            if (overlap(all[i], all[j])) return AP_ERR_ALIAS;
+    }
+    DeviceInfo di;
+    const ap_status st = current_device(&di);
+    if (st != AP_OK) return st;
+    return launch_block_scale(amax, scale, inv, n, stream);
+}
+
 ap_status ap_matmul_fp8(const uint8_t* a, int64_t lda, const float* a_scales, const uint8_t* b, int64_t ldb,
                         const float* b_scales, int b_block_rows, void* c, int64_t ldc, ap_dtype c_type, int64_t m,
                         int64_t n, int64_t k, cudaStream_t stream) {

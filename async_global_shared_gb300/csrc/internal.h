@@ -211,6 +211,7 @@ struct QuantArgs {
     int block_rows;
 };
 ap_status launch_quantize(const DeviceInfo& di, const QuantArgs& a, cudaStream_t stream);
+ap_status launch_block_scale(const float* amax, float* scale, float* inv, int64_t n, cudaStream_t stream);
 
 struct MatmulArgs {
     const uint8_t* a;

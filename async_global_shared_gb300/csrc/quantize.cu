@@ -198,7 +198,20 @@ ap_status launch_quant_t(const QuantArgs& a, cudaStream_t stream) {
                              : launch_early(quantize_tile_kernel<T, true>, grid, 256, stream, P);
 }
 
+__global__ void __launch_bounds__(256) block_scale_kernel(const float* amax, float* scale, float* inv, int64_t n) {
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= n) return;
+    const Scale s = scale_of(amax[i]);
+    scale[i] = s.s;
+    inv[i] = s.inv;
+}
+
 }  // namespace
+
+ap_status launch_block_scale(const float* amax, float* scale, float* inv, int64_t n, cudaStream_t stream) {
+    block_scale_kernel<<<static_cast<unsigned>((n + 255) / 256), 256, 0, stream>>>(amax, scale, inv, n);
+    return cudaGetLastError() == cudaSuccess ? AP_OK : AP_ERR_CUDA;
+}
 
 ap_status launch_quantize(const DeviceInfo&, const QuantArgs& a, cudaStream_t stream) {
     switch (a.type) {

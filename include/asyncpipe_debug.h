@@ -192,6 +192,13 @@ ap_status ap_debug_emulate_ring_tensor(const float* in_host, float* out_host, in
  */
 int64_t ap_debug_norm_grad_ctas(int64_t rows, int64_t cols, int type, int residual_type, int dresidual, int sms);
 
+/*
+ * The scale of blocks with these largest magnitudes, and its reciprocal, as the
+ * 8-bit operators' kernels compute them: scale[i] = max(amax[i] / 448, 2^-126),
+ * inv[i] = 1 / scale[i]. Device arrays of n floats, n at most 2^30.
+ */
+ap_status ap_debug_block_scale(const float* amax, float* scale, float* inv, int64_t n, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

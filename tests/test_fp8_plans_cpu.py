@@ -54,3 +54,11 @@ def test_give_up_setting(ap):
     for value in (16, 0):
         ap.ap_debug_set(ap.AP_DBG_GIVE_UP, value)
         assert ap.ap_debug_get(ap.AP_DBG_GIVE_UP) == value
+
+
+def test_block_scale_refusals(ap):
+    f = ap.load().ap_debug_block_scale
+    assert f(None, None, None, -1, None) == ap.AP_ERR_SHAPE and f(None, None, None, 0, None) == ap.AP_OK
+    assert f(None, 4096, 8192, 4, None) == ap.AP_ERR_NULL
+    assert f(2, 4096, 8192, 4, None) == ap.AP_ERR_ALIGN
+    assert f(4096, 4100, 8192, 4, None) == ap.AP_ERR_ALIAS
