@@ -62,3 +62,15 @@ def test_block_scale_refusals(ap):
     assert f(None, 4096, 8192, 4, None) == ap.AP_ERR_NULL
     assert f(2, 4096, 8192, 4, None) == ap.AP_ERR_ALIGN
     assert f(4096, 4100, 8192, 4, None) == ap.AP_ERR_ALIAS
+
+
+def test_no_device_behind_made_up_addresses(ap, request):
+    """Sessions without the GPU tests see no device, whatever the machine has."""
+    import os
+
+    import torch
+
+    assert not torch.cuda.is_available()
+    assert ap.load().ap_check(None) != ap.AP_OK
+    if request.config.option.markexpr.replace(" ", "") == "notgpu":
+        assert os.environ["CUDA_VISIBLE_DEVICES"] == ""
