@@ -167,7 +167,6 @@ __global__ void __launch_bounds__(Form<BN, CG, STAGES, PER_COL, SWAP>::kThreads,
     matmul_fp8_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
                       const __grid_constant__ CUtensorMap map_c, const __grid_constant__ MatmulParams P) {
     using F = Form<BN, CG, STAGES, PER_COL, SWAP>;
-    ptx::let_next_grid_start();
     constexpr int kCols = F::kCols;
     extern __shared__ unsigned char smem_raw[];
     __shared__ Shared<F, STAGES, PER_COL> sh;
@@ -211,6 +210,9 @@ __global__ void __launch_bounds__(Form<BN, CG, STAGES, PER_COL, SWAP>::kThreads,
     if (CG == 2) ptx::cluster_sync();  // the other CTA's barriers are ready too
     ptx::tcgen05_fence_after();
     const uint32_t tmem = sh.tmem;
+    // Only now that this grid has its tensor memory: a next grid that took some
+    // first and then waited for this one would keep it from starting.
+    ptx::let_next_grid_start();
     ptx::wait_previous_grid();  // nothing above touches global memory
 
     // A wait that gives up ends its role; the CTA's abort flag ends the

@@ -7,7 +7,7 @@ import torch
 import fp8_util as fu
 from fp8_util import TYPES, Strided, f64
 from gpu_util import device, lib, reset_debug
-from test_gpu_fp8 import check_matmul, done, operand
+from test_gpu_fp8 import check_matmul, done, operand, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -189,3 +189,27 @@ def test_pairs_bounded_wait(ap, tile):
     assert ap.ap_check() == ap.AP_OK
     reset_debug(ap)
     check_matmul(ap, m, n, k, tile, torch.float32)
+
+
+def test_products_between_the_library_s(ap):
+    """Kernels that hold tensor memory, this library's and torch's, one behind another in a stream: each product is what it
+    is alone, and none keeps another from starting."""
+    x, y = randn(512, 2048).bfloat16(), randn(2048, 512, seed=1).bfloat16()
+    big = randn(2048, 2048, seed=2).bfloat16()
+    cases, alone = [], []
+    for m, n, k in ((1, 8192, 4096), (16, 8192, 2048), (32, 8192, 4096), (64, 4096, 4096), (2048, 2560, 1024)):
+        cases.append((*operand(m, k, 1, m), *operand(n, k, 128, n), torch.empty(m, n, device="cuda")))
+        ap.ap_matmul_fp8(*cases[-1])
+        done(ap)
+        alone.append(cases[-1][-1].clone())
+    want = [x @ y, big @ big]
+    got = None
+    for _ in range(100):
+        for case in cases:
+            case[-1].fill_(float("nan"))
+            ap.ap_matmul_fp8(*case)
+            got = [x @ y, big @ big]
+            ap.ap_matmul_fp8(*case)
+    done(ap)
+    assert all(torch.equal(case[-1], c) for case, c in zip(cases, alone))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
