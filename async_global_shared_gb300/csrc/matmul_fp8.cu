@@ -645,7 +645,18 @@ ap_status launch_form(const DeviceInfo& di, MatmulParams P, const MatmulArgs& a,
     using F = Form<BN, CG, STAGES, PER_COL, SWAP>;
     static_assert(F::kCtas * (F::kSmem + sizeof(Shared<F, STAGES, PER_COL>) + 1024) <= kSmemPerSM, "shared memory of an SM");
     static_assert(F::kCtas * F::kTmemCols <= 512, "tensor memory of an SM");
-    static_assert(CG == 2 || F::kShareBytes <= F::kRingBytes, "a share fits in the ring");
+    static_assert(F::kTmemCols >= 32 && (F::kTmemCols & (F::kTmemCols - 1)) == 0, "columns that can be allocated");
+    static_assert(((F::kBuffers - 1) * F::kRun + F::kRun - 1) * BN + (F::kMmaGroups - 1) * F::kMmaCols + F::kMmaCols <= F::kTmemCols,
+                  "the last accumulator's last columns are allocated");
+    static_assert(F::kMmaCols % 16 == 0 && F::kMmaCols <= 256 && F::kCols % 16 == 0, "columns of an instruction, of a load");
+    static_assert(F::kPBytes % 1024 == 0 && F::kQBytes % 1024 == 0 && F::kStageBytes % 1024 == 0, "operands start on swizzle atoms");
+    static_assert(F::kQBox <= 256 && F::kQBox * CG * F::kMmaGroups == BN, "boxes cover the tile's columns");
+    static_assert(1023 + F::kRingBytes + F::kStagingBytes <= F::kSmem, "ring and staging from the first 1024-byte boundary on");
+    static_assert(CG == 2 || (SWAP ? size_t(BN) * kTile * 4 : F::kShareBytes) <= F::kRingBytes, "a share fits in the ring");
+    static_assert(F::kShareBytes >= ((kTile - 1) * size_t(F::kSharePitch) + BN) * 4, "a share's last value");
+    static_assert(sizeof(Shared<F, STAGES, PER_COL>::col_scales[0][0]) % 16 == 0 &&
+                      sizeof(Shared<F, STAGES, PER_COL>::col_scales[0][0]) >= 4 * size_t(PER_COL ? F::kGroups * F::kCols : F::kGroups),
+                  "a block's column scales, in whole 16-byte loads");
     P.np = SWAP ? a.n : a.m;
     P.nq = SWAP ? a.m : a.n;
     P.p_scales = SWAP ? a.b_scales : a.a_scales;
