@@ -1,6 +1,8 @@
 // Root-mean-square norm with the residual's addition and an output in 16/32
 // bits and / or e4m3. For a row of N values:
-//     h = x + residual,  r = 1 / sqrt(sum(h^2) / N + eps),  y = h r w.
+//     h = x + residual,  r = 1 / sqrt(sum(h^2) / N + eps),  y = (h r) w.
+// h r is of the order of 1 whatever the row's and the weight's sizes; r w need
+// not be a float.
 // The sum comes before the first output, so a row is held in registers between
 // the two and memory is passed over once. Memory bounds it: 32768 x 8192 bf16
 // with a 32-bit residual, e4m3 out, 432 us = 6.85 TB/s; 16384 x 8192 with a bf16
@@ -136,7 +138,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) rms_norm_kernel(const __gri
         float w[8];
         take_weight<SPREAD, T>(a.weight, a.weight_type == a.type, col + c * apart, left - c * apart, w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) h[c][i] *= r * w[i];
+        for (int i = 0; i < 8; ++i) h[c][i] = h[c][i] * r * w[i];
     }
     write_row<T, C, SPREAD>(P, row, col, apart, h);
 }
@@ -230,7 +232,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
                 if (!kKeep && left > c * apart) again_weight<T, W, SPREAD>(P, weights, col + c * apart, left - c * apart, again);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    if (kKeep || left > c * apart) h[c][i] *= r * (kKeep ? w[kKeep ? c : 0][i] : again[i]);
+                    if (kKeep || left > c * apart) h[c][i] = h[c][i] * r * (kKeep ? w[kKeep ? c : 0][i] : again[i]);
             }
             write_row<T, C, SPREAD>(P, row, col, apart, h);
         }
@@ -283,7 +285,7 @@ __global__ void __launch_bounds__(1024) rms_norm_wide_kernel(const __grid_consta
         else
             load8(static_cast<const float*>(a.weight) + col, P.vec_w, a.cols - col).unpack(w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) h[0][i] *= r * w[i];
+        for (int i = 0; i < 8; ++i) h[0][i] = h[0][i] * r * w[i];
         write_row<T, 1, false, true>(P, row, col, 0, h);
     }
 }

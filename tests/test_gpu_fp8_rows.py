@@ -7,7 +7,7 @@ import torch
 import fp8_util as fu
 from fp8_util import TYPES, U, f64
 from gpu_util import device, lib, reset_debug
-from test_gpu_fp8 import E4M3, check_grad, done, grad_case, randn
+from test_gpu_fp8 import E4M3, check_grad, done, empty8, grad_case, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -104,3 +104,19 @@ def test_norm_backward_forms_past_2_31_elements(ap, path, form):
         terms += p.abs().sum(0)
     # a CTA adds at most ceil(rows / 152) rows one after another, the partials' sum 304 more
     assert bool(((dw.double() - sums).abs() <= (rows // 152 + 320) * U * terms).all().item())
+
+
+@pytest.mark.parametrize("rows,cols", [(3, 200), (2, 1000), (2, 5000), (2, 40001), (3, 4099), (700, 1024), (700, 1023)])
+@pytest.mark.parametrize("size,weight", [(1e16, 1e-25), (1e-15, 1e25), (1e-17, 1e30), (1e15, 1e-30)])
+def test_norm_of_large_rows_with_small_weights(ap, rows, cols, size, weight):
+    """h r is of the order of 1; r times the weight is subnormal or past the largest float."""
+    x, w = size * randn(rows, cols), weight * (1 + 0.1 * randn(cols, seed=1))
+    _, rr, yy = fu.norm(f64(x), None, f64(w), 0.0)
+    rel = (fu.DEPTH / 2 + 8) * U
+    for path in (1, 2):
+        ap.ap_debug_set(ap.AP_DBG_FORCE_PATH, path)
+        y, q, s = torch.empty_like(x), empty8(rows, cols), torch.empty(rows, fu.blocks(cols), device="cuda")
+        ap.ap_rms_norm(x, w, 0.0, y=y, q=q, q_scales=s)
+        done(ap)
+        assert np.all(np.abs(f64(y) - yy) <= rel * np.abs(yy) + U * np.abs(yy))
+        fu.check_codes(q, s, yy, 1, rel, "norm")
