@@ -21,6 +21,20 @@ struct NormParams {
     int64_t blocks;                          // scales of a row
 };
 
+// Zeros past the row's end, `left` columns from the thread's first one, for an
+// infinite r (no eps, and squares that all vanish): 0 r would be NaN there, and
+// a block's amax takes in what lies past the end. (Of whole rows a chunk lies
+// in the row or past it: write_row looks.)
+template <int C, bool SPREAD>
+__device__ __forceinline__ void clear_past_end(float r, int64_t left, int64_t step, float (&y)[C][8]) {
+    if (r <= 3.402823466e38f) return;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (c * step + (SPREAD ? 32 * i : i) >= left) y[c][i] = 0.0f;
+}
+
 // What is written of a row's y, C chunks a thread `step` columns apart, the
 // first at col. A block's 128 values lie in the 16 lanes of a half warp, its
 // amax four shuffles away (SPREAD: four in each lane of the warp, five
@@ -51,7 +65,7 @@ __device__ __forceinline__ void write_row(const NormParams& P, int64_t row, int6
                 m[c][0] = amax3(amax3(y[c][0], y[c][1], y[c][2]), y[c][3], 0.0f);
                 m[c][kPer - 1] = amax3(amax3(y[c][4], y[c][5], y[c][6]), y[c][7], 0.0f);
             } else {
-                m[c][0] = amax8(y[c]);
+                m[c][0] = RAGGED || c * step < left ? amax8(y[c]) : 0.0f;
             }
         }
 #pragma unroll
@@ -140,6 +154,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) rms_norm_kernel(const __gri
 #pragma unroll
         for (int i = 0; i < 8; ++i) h[c][i] = h[c][i] * r * w[i];
     }
+    if (SPREAD) clear_past_end<C, SPREAD>(r, left, apart, h);
     write_row<T, C, SPREAD>(P, row, col, apart, h);
 }
 
@@ -234,6 +249,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
                 for (int i = 0; i < 8; ++i)
                     if (kKeep || left > c * apart) h[c][i] = h[c][i] * r * (kKeep ? w[kKeep ? c : 0][i] : again[i]);
             }
+            if (SPREAD) clear_past_end<C, SPREAD>(r, left, apart, h);
             write_row<T, C, SPREAD>(P, row, col, apart, h);
         }
         s += groups;
@@ -286,6 +302,7 @@ __global__ void __launch_bounds__(1024) rms_norm_wide_kernel(const __grid_consta
             load8(static_cast<const float*>(a.weight) + col, P.vec_w, a.cols - col).unpack(w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) h[0][i] = h[0][i] * r * w[i];
+        clear_past_end<1, false>(r, a.cols - col, 0, h);
         write_row<T, 1, false, true>(P, row, col, 0, h);
     }
 }

@@ -120,3 +120,20 @@ def test_norm_of_large_rows_with_small_weights(ap, rows, cols, size, weight):
         done(ap)
         assert np.all(np.abs(f64(y) - yy) <= rel * np.abs(yy) + U * np.abs(yy))
         fu.check_codes(q, s, yy, 1, rel, "norm")
+
+
+@pytest.mark.parametrize("rows,cols", [(3, 7), (3, 200), (2, 1000), (2, 5000), (2, 40001), (3, 4099), (700, 1032), (700, 1023)])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_norm_of_rows_whose_squares_vanish(ap, rows, cols, kind):
+    """No eps and squares below the smallest float: r is infinite and so is every y; the last block of a row, which may be
+    short, is one of infinities like the others."""
+    x = (1e-25 * (1 + torch.rand(rows, cols, device="cuda"))).to(TYPES[kind])
+    w = torch.ones(cols, device="cuda")
+    for path in (1, 2):
+        ap.ap_debug_set(ap.AP_DBG_FORCE_PATH, path)
+        y, q = torch.empty_like(x), empty8(rows, cols)
+        s, r = torch.zeros(rows, fu.blocks(cols), device="cuda"), torch.empty(rows, device="cuda")
+        ap.ap_rms_norm(x, w, 0.0, y=y, q=q, q_scales=s, rstd=r)
+        done(ap)
+        assert torch.isposinf(r).all() and torch.isposinf(y).all() and torch.isposinf(s).all()
+        assert torch.isnan(q.float()).all()
