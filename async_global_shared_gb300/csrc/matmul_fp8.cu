@@ -25,13 +25,16 @@
 //
 // What bounds it. One token times 8192 x 8192: the weight's bytes, 14.9 us = 4.5
 // TB/s, of which 5 are the launch, the first loads and the reduction (8 tokens
-// times 28672 x 8192: 39 us = 6.0 TB/s). 128 x 128 tiles: shared memory, 512
-// cycles a block (333 x 4104 x 5000: 18.6 us). 8192^3 in pairs: 440 us = 2.5
+// times 28672 x 8192: 39 us = 6.0 TB/s). 128 x 128 tiles: the consumers'
+// instructions, 66 % of the issue slots over a CTA's life, beside 512 cycles a
+// block of shared memory, 59 % (333 x 4104 x 5000: 18.6 us, a quarter of it
+// launch, first loads and exit). 8192^3 in pairs: 440 us = 2.5
 // PFLOP/s, 410 before the power limit lowers the clocks (596 with one CTA a
 // 128 x 128 tile): the consumers, whose loads, sums and hand-over of a block
 // take about 850 cycles beside 512 of matrix instructions. Scales by column on
 // top: two operations a value, and the column scales' loads (4096 x 8192 x
-// 16384: 701 us = 1.57 PFLOP/s; 599 without the loads).
+// 16384: 701 us = 1.57 PFLOP/s; 599 without the loads; with c in 32 bits, as
+// here, 56 bytes of spills a thread).
 //
 // Roles in a CTA, each a warp: the producer streams the operands' 128-byte
 // wide boxes through a ring of shared-memory stages (tensor maps, 128-byte

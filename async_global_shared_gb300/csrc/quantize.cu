@@ -49,7 +49,9 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const __grid_constan
 // instructions, so maxima are taken two 16-bit values at a time, eight rows'
 // maxima cross 16 lanes in eight exchanges (each halves the rows a lane still
 // carries, so a row's scale is computed by two lanes and not by 16), and both
-// outputs' codes come from one unpacking.
+// outputs' codes come from one unpacking. (Float by tiles: 34 % of the issue
+// slots and 58 % of DRAM's peak; 98 registers leave two CTAs an SM, whose waits
+// for their loads bound it.)
 template <typename T, bool TILES>
 __global__ void __launch_bounds__(256) quantize_tile_kernel(const __grid_constant__ QuantParams P) {
     using K = Peak<T>;

@@ -6,9 +6,9 @@
 // The sum comes before the first output, so a row is held in registers between
 // the two and memory is passed over once. Memory bounds it: 32768 x 8192 bf16
 // with a 32-bit residual, e4m3 out, 432 us = 6.85 TB/s; 16384 x 8192 with a bf16
-// residual 144 us; 1237 x 5000 f16, both outputs, 8.6 us; one row of 4096 2.3 us
-// on the device. Rows off the 16-byte boundaries move element by element, where
-// instructions bound it: 27513 x 3163 f16 with a 32-bit residual 225 us = 4.3
+// residual 151 us; 1237 x 5000 f16, both outputs, 9.2 us in a graph; one row of
+// 4096 2.1. Rows off the 16-byte boundaries move element by element, where
+// instructions bound it: 27513 x 3163 f16 with a 32-bit residual 223 us = 4.3
 // TB/s.
 #include "row_ring.cuh"
 
@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) rms_norm_kernel(const __gri
 // The ring's form: teams of warps, rows from shared memory, the weight in
 // registers for the whole grid's life (four chunks: in shared memory). One row a
 // CTA leaves the memory idle while the row's sum is on its way: 16384 x 8192
-// took 235 us so, 144 with the ring.
+// took 235 us so, 151 with the ring.
 template <typename T, typename R, int C, bool RES, Weights W, bool SPREAD>
 __global__ void __launch_bounds__(kRingThreads, 1)
     rms_norm_ring_kernel(const __grid_constant__ NormParams P, const __grid_constant__ RowRing ring) {
@@ -359,7 +359,11 @@ ap_status launch_norm_t(const DeviceInfo& di, const Options& o, const NormArgs& 
     // CTA's one or two wide teams then wait on their sums with nothing else to
     // do (no residual, y in f16: 9728 x 12000 107 us against 95 in registers,
     // 9728 x 6000 55 against 49; with two teams of four chunks 9728 x 8192 63
-    // against 71; with a residual 145 against 205 at 9728 x 12000).
+    // against 71; with a residual 145 against 205 at 9728 x 12000). The same for
+    // other types and outputs: 9728 x 12000 bf16 to e4m3 120 against 91, f32 to
+    // e4m3 123 against 107, 9728 x 6000 62 and 51, 63 and 57, rows off the
+    // boundaries (9728 x 6001 bf16 to e4m3) 80 and 72. f32 with y in f32, DRAM's
+    // alone, is the same either way (161 and 160; 16384 columns 219 and 231).
     const auto idle = [&] { return o.force_path != 1 && !res && (ring.teams == 1 || (ring.teams == 2 && ring.chunks == 3)); };
     if (many && plan_ring(di, o, &ring, res ? 2 : 1, in, ld, size, nullptr, a.rows, a.cols, whole) && !idle()) {
         const int64_t grid = ring_grid(ring, di.sms, o.grid);
