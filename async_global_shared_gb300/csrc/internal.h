@@ -284,10 +284,6 @@ ap_status launch_gated_grad(const DeviceInfo& di, const GatedGradArgs& a, cudaSt
 // Largest chunk accepted by ap_cluster_exchange for this much shared memory.
 constexpr int64_t kSmemOptinGB300 = 232448;  // 227 KiB per CTA on compute capability 10.x
 constexpr int64_t kSmemPerSM = 233472;       // 228 KiB per SM
-// Shared memory a CTA may take, its reserve included, that runs two an SM and
-// may have a two-CTA form of the 8-bit product start beside it (102 KiB at most):
-// their sum stays below the 208 KiB of matmul_fp8.cuh's kOperandLimit.
-constexpr int64_t kSmemBeside = 106 * 1024;
 constexpr int64_t kRollSmallMaxBytes = 32 * 1024;
 
 }  // namespace ap

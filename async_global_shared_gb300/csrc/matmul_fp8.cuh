@@ -23,9 +23,9 @@
 // sums its share, and the shares are added through distributed shared memory
 // in rank order.
 //
-// What bounds it. One token times 8192 x 8192: the weight's bytes, 14.9 us = 4.5
+// What bounds it. One token times 8192 x 8192: the weight's bytes, 14.5 us = 4.6
 // TB/s, of which 5 are the launch, the first loads and the reduction (8 tokens
-// times 28672 x 8192: 39 us = 6.0 TB/s). 128 x 128 tiles: the consumers'
+// times 28672 x 8192: 40.5 us = 5.8 TB/s). 128 x 128 tiles: the consumers'
 // instructions, 66 % of the issue slots over a CTA's life, beside 512 cycles a
 // block of shared memory, 59 % (333 x 4104 x 5000: 18.6 us, a quarter of it
 // launch, first loads and exit). 8192^3 in pairs: 440 us = 2.5
@@ -63,11 +63,12 @@ constexpr int kMaxSplit = 8;
 constexpr int kScaleRun = 8;    // blocks of k whose scales are brought at once (one 32-byte sector of a row)
 constexpr int kScaleSlots = 2;  // such runs in shared memory
 // Where in an SM's shared memory (kSmemPerSM) matrix instructions' operands may
-// end. A gated form with two CTAs of 106 KB an SM raised an illegal address (1 x
-// 8192 x 2048, 256 CTAs in clusters of four); with one CTA an SM it does not. Two
-// forms of the plain product faulted alike, two CTAs of 111 KB an SM, while those
-// that are left, two of 102 KB at most, never did. What the faults have in common is
-// operands past the first 208 KB; the cause itself was not established.
+// end. Three forms that are out of the tree raised an illegal address, two CTAs of
+// 106 to 112 KB an SM each (a gated one at 1 x 8192 x 2048, 256 CTAs in clusters of
+// four; two of 64 accumulator columns), while two CTAs of 102 KB an SM never did.
+// Operands past the first 208 KB are what the three have in common. That is a
+// correlation: the cause was not established. Every form keeps clear of it
+// wherever on an SM its CTA starts, beside whatever other CTAs (see kTailBytes).
 constexpr size_t kOperandLimit = 208 * 1024;
 constexpr int64_t kMaxTiles = int64_t(1) << 27;  // tile numbers plus a grid, times a cluster, stay in 32 bits
 
@@ -134,16 +135,16 @@ struct Form {
     static constexpr int kBuffers = CG == 2 ? 512 / BN : 2;
     static constexpr uint32_t kTmemCols = kBuffers * kRun * kAccCols;
     // CTAs an SM: the narrow forms wait more than they compute. Of the gated
-    // ones, whose stages are twice as large, two would end past kOperandLimit.
+    // ones, whose stages are twice as large, two do not fit.
     static constexpr int kCtas = SWAP && !GATED ? 2 : 1;
     // c leaves through shared memory: a consumer warp's 32 rows of 128 bytes
     static constexpr bool kPeaks = GATED && CG == 2;
     static constexpr bool kStaged = !SWAP && !(GATED && CG == 1);
     static constexpr uint32_t kStagingBytes = kStaged ? 32 * 128 * kConsumerWarps : 0;
     static constexpr size_t kRingBytes = size_t(STAGES) * kStageBytes;
-    // unused room behind a gated form's ring: wherever on an SM, beside whatever
-    // else, such a CTA starts, its operands end below kOperandLimit
-    static constexpr uint32_t kTailBytes = GATED && !kStaged ? kSmemPerSM - kOperandLimit : 0;
+    // unused room behind the ring where no staging is: wherever on an SM, beside
+    // whatever else, a CTA starts, its operands end below kOperandLimit
+    static constexpr uint32_t kTailBytes = kStaged ? 0 : kSmemPerSM - kOperandLimit;
     static constexpr size_t kSmem = kRingBytes + kStagingBytes + kTailBytes + 1024;
     // a split tile's shares: rows of BN floats, padded so that the 32 rows a
     // warp writes fall on different banks; or columns of 128 floats
@@ -901,9 +902,7 @@ constexpr bool checked() {
     using F = Form<BN, CG, STAGES, PER_COL, SWAP, GATED>;
     static_assert(F::kCtas * (F::kSmem + sizeof(Shared<F, STAGES, PER_COL>) + 1024) <= kSmemPerSM, "shared memory of an SM");
     static_assert(F::kSmem + sizeof(Shared<F, STAGES, PER_COL>) <= kSmemOptinGB300, "shared memory of a CTA");
-    static_assert(F::kCtas * (F::kSmem + sizeof(Shared<F, STAGES, PER_COL>) + 1024) - F::kStagingBytes - F::kTailBytes <= kOperandLimit,
-                  "operands end below what was seen to work");
-    static_assert(!GATED || kSmemPerSM - (F::kStagingBytes + F::kTailBytes) <= kOperandLimit, "also beside other CTAs");
+    static_assert(kSmemPerSM - (F::kStagingBytes + F::kTailBytes) <= kOperandLimit, "operands end below what was seen to work, beside any CTA");
     static_assert(F::kCtas * F::kTmemCols <= 512, "tensor memory of an SM");
     static_assert(F::kTmemCols >= 32 && (F::kTmemCols & (F::kTmemCols - 1)) == 0, "columns that can be allocated");
     static_assert(F::kMmaGroups * F::kMmaCols * F::kHalves == F::kAccCols && F::kBuffers * F::kRun * F::kAccCols <= F::kTmemCols,

@@ -45,11 +45,6 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kRows = 16;  // of a row tile
 constexpr int kMaxSplit = 8;
-// Shared memory of a CTA such that beside one or two of them no CTA of the 8-bit
-// product (93 or 102 KiB) ends past kOperandLimit (matmul_fp8.cuh): at least
-// kSmemLeast, so that none fits behind two; at most kSmemBeside, or at least
-// kSmemAlone, so that none fits behind one.
-constexpr int64_t kSmemLeast = 70 * 1024, kSmemAlone = 136 * 1024;
 
 struct W4Params {
     const void* x;
@@ -155,7 +150,7 @@ struct Form {
     static constexpr int kTurns = kRows * kUnits / 32; // copies a lane and weight
     static constexpr int kCtas = NT == 4 || (GATED && STEPS == 1) ? 1 : 2;  // an SM: what their registers allow
     static constexpr int kStages = NT == 1 && kCtas == 2 && kStrands == 2 ? 2 : 4;
-    static constexpr int64_t kSmemMost = kCtas == 1 ? kSmemOptinGB300 : kSmemBeside - 1024;
+    static constexpr int64_t kSmemMost = kCtas == 1 ? kSmemOptinGB300 : kSmemPerSM / 2 - 1024;
     static constexpr int kRingBytes = kWarps * kStages * kStrands * kTileBytes;
     static constexpr int kXRows = 8 * NT;
     // shares of a CTA's sums: [part][output][x row][weight row]
@@ -500,8 +495,7 @@ bool plan_smem(W4Params& P, int64_t xrows, int64_t* bytes) {
     // stretches of about the same length
     const int64_t stretches = (mine + fits - 1) / fits;
     P.stretch = static_cast<int>((mine + stretches - 1) / stretches);
-    *bytes = std::max<int64_t>({fixed + P.stretch * per_block, F::kShareBytes, kSmemLeast});
-    if (*bytes > kSmemBeside - 1024) *bytes = std::max(*bytes, kSmemAlone);
+    *bytes = std::max<int64_t>(fixed + P.stretch * per_block, F::kShareBytes);
     return *bytes <= kSmemOptinGB300;
 }
 
