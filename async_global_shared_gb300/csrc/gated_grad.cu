@@ -211,6 +211,14 @@ struct Kept {
     }
 };
 
+// The first n (may be negative) of eight codes, zeros after them: past a matrix's
+// last column also in a block whose 1 / s is NaN.
+__device__ __forceinline__ uint2 first_codes(uint2 w, int64_t n) {
+    if (n >= 8) return w;
+    const uint64_t keep = n > 0 ? ~uint64_t(0) >> (64 - 8 * n) : 0;
+    return make_uint2(w.x & static_cast<uint32_t>(keep), w.y & static_cast<uint32_t>(keep >> 32));
+}
+
 constexpr int kTurned = kScaleBlock * 16 * 8;  // bytes of a tile's transposed codes
 
 struct TileShared {
@@ -357,7 +365,9 @@ __device__ __forceinline__ void tile_grad(const GradParams& P, unsigned char* sm
             if (by_rows && p + r < rows) {
                 const float2 inv = *reinterpret_cast<const float2*>(sh.row_inv[8 * rows8 + p + r]);
                 uint8_t* q = a.q + (row0 + p + r) * a.ldq + col;
-                store_codes(q, WHOLE || P.vec_q, 8, codes8(dg[r], inv.x));  // up to du's first column: zeros past dg's last
+                uint2 w = codes8(dg[r], inv.x);
+                if (!WHOLE) w = first_codes(w, cols);
+                store_codes(q, WHOLE || P.vec_q, 8, w);  // up to du's first column: zeros past dg's last
                 if (cols > 0) store_codes(q + half, WHOLE || P.vec_q, cols, codes8(du[r], inv.y));
             }
         }
