@@ -10,8 +10,8 @@
 //    tiles) and every so manieth block of 256 or 128 columns, and streams those codes
 //    through a ring of shared memory of its own, by 16-byte asynchronous copies
 //    (128 or 64 bytes a row and block): no barrier is needed before the end.
-//  - A word of a row holds eight columns; a shift and a mask bring columns i
-//    and i + 4 at once into a pair of 16-bit numbers 16 + code (see Codes).
+//  - A word of a row holds eight columns; shifts, masks and a subtraction bring columns i
+//    and i + 4 at once into a pair of 16-bit numbers code - zero (see Codes).
 //  - The products run on the warp's matrix instruction m16n8k16 with the
 //    weight's rows on its 16 rows and the rows of x on its 8 columns, so up to
 //    8 rows of x cost what one costs. (tcgen05 would want the widened codes
@@ -20,15 +20,15 @@
 //    eight of its values in the order 0 4 1 5 2 6 3 7, which is how the codes
 //    come out of a word.
 //  - A group's products are summed by themselves and then scaled, in 32 bits.
-//  - x and its groups' sums are staged for a stretch of blocks at a time.
+//  - x is staged for a stretch of blocks at a time.
 //  - The warps of a CTA share the staged x. Where that leaves few CTAs a cluster
 //    shares k, and adds its shares through distributed shared memory in rank
 //    order.
 // It measured (the codes at the rate of a copy would take 5.1, 10.2 and 11 us): one row
-// times 8192 x 8192 12.6 us, gated times 16384 x 4096 20, 32 rows times 8192 x 16384
-// 64. What bounds it then are instructions: about 300 for 256 columns of 16 rows, 128
-// of them the widening, and a thousand a warp around them; with two CTAs of eight
-// warps an SM the issue slots are 40 to 55 % busy, and waits on the ring, the
+// times 8192 x 8192 13.0 us, gated times 16384 x 4096 20.9, 32 rows times 8192 x 16384
+// 59.7. What bounds it then are instructions, half of them the widening (11 for a word's
+// eight codes in bf16, 9 in fp16), and a thousand a warp around them; with two CTAs of
+// eight warps an SM the issue slots are about half busy, and waits on the ring, the
 // matrix instructions and one another take the rest.
 #include <algorithm>
 #include <atomic>
@@ -73,18 +73,50 @@ __device__ __forceinline__ float lds4(uint32_t addr) {
 }
 __device__ __forceinline__ void sts4(uint32_t addr, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory"); }
 
-// A code v as a 16-bit number 16 + v: v on the four highest mantissa bits of
-// 16. That takes a shift and a mask for two codes, and no subtraction: what is
-// too much, 16 + zero times the group's sum of x, is taken off the group's sum
-// in 32 bits. (An offset of 16 costs two or three of the sum's 24 bits; the
-// plainer patterns, 128 + v in bf16 and 1024 + v in fp16, would cost five and
-// eight, or a subtraction for every two codes.)
+// (w & mask) | power
+__device__ __forceinline__ uint32_t code_of(uint32_t w, uint32_t mask, uint32_t power) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(power));
+    return r;
+}
+
+// A word's eight codes as 16-bit numbers code - zero, pairs of columns (0, 4), (1, 5),
+// (2, 6), (3, 7), exact for every code and zero point: a mask puts a code on the lowest
+// mantissa bits of a power of two (128 in bf16, 1024 in fp16), and the power and the
+// zero point are taken off in one operation for two codes. (A form whose products are of
+// x and 16 + code and which takes 16 + zero times the group's sum of x off the group's
+// sum saves that operation, but its sums lose what the correction cancels: a large x
+// where code = zero, all x of one sign, an infinity. It measured 12.6, 20.4 and 63.8 us
+// for the three above: it has to take and keep the sums of x.)
 template <typename T>
 struct Codes;
 template <>
 struct Codes<__nv_bfloat16> {
-    static constexpr uint32_t kMask = 0x00780078u, kSixteen = 0x41804180u;
-    static constexpr int kAt = 3;
+    // bf16 has every whole number up to 256: of a zero point above 128 the first 128
+    // are taken off with the power, the rest by a second subtraction.
+    struct Zero {
+        uint32_t first, rest;  // 128 + the first, twice; the rest
+    };
+    static constexpr uint32_t kPower = 0x43004300u;  // 128
+    static __device__ __forceinline__ bool large(uint32_t zero) { return zero > 128; }
+    static __device__ __forceinline__ uint32_t sub(uint32_t a, uint32_t b) {
+        uint32_t r;
+        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
+    static __device__ __forceinline__ Zero zero_of(uint32_t zero) {
+        const uint32_t low = min(zero, 128u);
+        return Zero{(0x4300u + low) * 0x10001u, zero - low};
+    }
+    static __device__ __forceinline__ void widen(uint32_t w, uint32_t mask, uint32_t power, const Zero& z, bool large, uint32_t (&p)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] = sub(code_of(w >> (4 * i), mask, power), z.first);
+        if (large) {
+            const uint32_t rest = sub((0x4300u + z.rest) * 0x10001u, kPower);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) p[i] = sub(p[i], rest);
+        }
+    }
     // d += (first: =) a * b
     static __device__ __forceinline__ void mma(float (&d)[4], bool first, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                                uint32_t b1) {
@@ -100,8 +132,31 @@ struct Codes<__nv_bfloat16> {
 };
 template <>
 struct Codes<__half> {
-    static constexpr uint32_t kMask = 0x03C003C0u, kSixteen = 0x4C004C00u;
-    static constexpr int kAt = 6;
+    // Codes on bits 0 to 3 as 1024 + code, those on bits 4 to 7 as 1024 + 16 code, a
+    // sixteenth of which less 64 + zero is one fused operation; every number is whole
+    // and below 2048.
+    struct Zero {
+        uint32_t first, second;  // 1024 + zero, -(64 + zero)
+    };
+    static constexpr uint32_t kPower = 0x64006400u;  // 1024
+    static __device__ __forceinline__ bool large(uint32_t) { return false; }
+    static __device__ __forceinline__ uint32_t sub(uint32_t a, uint32_t b) {
+        uint32_t r;
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
+    static __device__ __forceinline__ Zero zero_of(uint32_t zero) {
+        const uint32_t first = (0x6400u + zero) * 0x10001u;
+        return Zero{first, sub(0x63806380u, first)};  // 960 - (1024 + zero)
+    }
+    static __device__ __forceinline__ void widen(uint32_t w, uint32_t mask, uint32_t power, const Zero& z, bool, uint32_t (&p)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+            const uint32_t v = w >> (4 * i);
+            p[i] = sub(code_of(v, mask, power), z.first);
+            asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(p[i + 1]) : "r"(code_of(v, mask << 4, power)), "r"(0x2C002C00u), "r"(z.second));
+        }
+    }
     // d += (first: =) a * b
     static __device__ __forceinline__ void mma(float (&d)[4], bool first, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                                uint32_t b1) {
@@ -116,25 +171,12 @@ struct Codes<__half> {
     }
 };
 
-// A word's eight codes as 16 + code, pairs of columns (0, 4), (1, 5), (2, 6), (3, 7).
-template <typename T>
-__device__ __forceinline__ void widen(uint32_t w, uint32_t mask, uint32_t sixteen, uint32_t (&p)[4]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int by = 4 * i - Codes<T>::kAt;
-        asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(p[i]) : "r"(by < 0 ? w << -by : w >> by), "r"(mask), "r"(sixteen));  // (a & b) | c
-    }
-}
-
-// 16 + a zero point, by way of 2^23 + it.
-__device__ __forceinline__ float sixteen_and(uint32_t zero) { return __uint_as_float(0x4B000000u | zero) - (8388608.0f - 16.0f); }
-
 // Weights side by side, 8-row tiles of x, and what they take of shared memory.
 template <int NT, bool GATED, int STEPS>
 struct Form {
     // A warp's strands of 16 rows, which share what it loads of x: the same rows
     // of two weights (gated), or for more than 8 rows of x two row tiles of one
-    // (32 x 8192 x 16384: 64 us, 72 with one; the other way 1 x 8192 x 8192 12.6, 13.4
+    // (32 x 8192 x 16384: 60 us, 72 with one at the time; the other way 1 x 8192 x 8192 12.6, 13.4
     // with two, whose ring is shorter).
     static constexpr int kStrands = GATED || NT > 1 ? 2 : 1;
     static constexpr int kOutputs = GATED ? 2 : 1;                        // sums a result takes
@@ -184,7 +226,6 @@ __global__ void __launch_bounds__(32 * kWarps, (Form<NT, GATED, STEPS>::kCtas)) 
     const uint32_t xpitch = static_cast<uint32_t>(stretch) * (2 * kBlock) + 64;
     const int srows = tiles * F::kWarpRows;  // weight rows of the CTA
     auto row_of = [&](int w, int r) { return row0 + tile * F::kWarpRows + (GATED ? 0 : w * kRows) + r; };  // of a strand
-    const uint32_t sums = xs + static_cast<uint32_t>(xrows) * xpitch;  // of x over a group: [group][x row]
 
     ptx::let_next_grid_start();
     ptx::wait_previous_grid();
@@ -274,15 +315,14 @@ __global__ void __launch_bounds__(32 * kWarps, (Form<NT, GATED, STEPS>::kCtas)) 
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[w][j][i] = 0.0f;
 
-    uint32_t mask = H::kMask, sixteen = H::kSixteen;  // in registers
-    asm volatile("" : "+r"(mask), "+r"(sixteen));
+    uint32_t mask = 0x000F000Fu, power = H::kPower;  // in registers
+    asm volatile("" : "+r"(mask), "+r"(power));
     // Where this lane reads, as pointers: their constant parts become offsets
     // of the loads. Of rows of x past the last one the last (the results are dropped).
     const unsigned char* const words_at = smem_raw + (ring - smem) + g * kPitch + 4 * t;
     const unsigned char* x_at[NT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) x_at[j] = smem_raw + (xs - smem) + min(8 * j + g, xrows - 1) * xpitch + 16 * t;
-    const unsigned char* const sums_at = smem_raw + (sums - smem) + 8 * t;
 
     // Those of a block's groups, fetched for the next block as soon as this
     // one's are used.
@@ -324,9 +364,8 @@ __global__ void __launch_bounds__(32 * kWarps, (Form<NT, GATED, STEPS>::kCtas)) 
     for (int s0 = b0; s0 < b1; s0 += stretch) {
         const int s1 = min(s0 + stretch, b1);
         if (s0 > b0) __syncthreads();
-        // x as it stands, then each thread puts its own units in order and takes
-        // the groups' sums
-        const int units = (s1 - s0) * (kBlock / 8);  // of a row; whole half warps
+        // x as it stands, then each thread puts its own units in order
+        const int units = (s1 - s0) * (kBlock / 8);  // of a row
         if (s0 > b0) {
             stage_x(s0, units);
             ptx::cp_async_commit();
@@ -334,27 +373,14 @@ __global__ void __launch_bounds__(32 * kWarps, (Form<NT, GATED, STEPS>::kCtas)) 
         } else {
             ptx::cp_async_wait_group<F::kStages - 1>();  // all but the ring's
         }
-        // the same lanes' own units; whole half warps
         const bool one = xrows == 1;
 #pragma unroll 1
         for (int r = one ? 0 : warp; r < xrows; r += kWarps) {
-            unsigned char* const row = smem_raw + (xs - smem) + r * xpitch;
+            uint4* const row = reinterpret_cast<uint4*>(smem_raw + (xs - smem) + r * xpitch);
 #pragma unroll 1
-            for (int c = one ? threadIdx.x : lane; c - lane < units; c += one ? 32 * kWarps : 32) {
-                const bool in = c < units;
-                Raw8<T> raw;
-                raw.w = make_uint4(0, 0, 0, 0);
-                if (in) raw.w = *reinterpret_cast<const uint4*>(row + 16 * c);
-                const uint4 w = raw.w;
-                if (in)
-                    *reinterpret_cast<uint4*>(row + 16 * c) =
-                        make_uint4(prmt(w.x, w.z, 0x5410), prmt(w.x, w.z, 0x7632), prmt(w.y, w.w, 0x5410), prmt(w.y, w.w, 0x7632));
-                float v[8];
-                raw.unpack(v);
-                float sum = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
-#pragma unroll
-                for (int o = 1; o < 4 * STEPS; o *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                if (in && (c & (4 * STEPS - 1)) == 0) sts4(sums + 4u * static_cast<uint32_t>(c / (4 * STEPS) * F::kXRows + r), sum);
+            for (int c = one ? threadIdx.x : lane; c < units; c += one ? 32 * kWarps : 32) {
+                const uint4 w = row[c];
+                row[c] = make_uint4(prmt(w.x, w.z, 0x5410), prmt(w.x, w.z, 0x7632), prmt(w.y, w.w, 0x5410), prmt(w.y, w.w, 0x7632));
             }
         }
         __syncthreads();
@@ -371,9 +397,22 @@ __global__ void __launch_bounds__(32 * kWarps, (Form<NT, GATED, STEPS>::kCtas)) 
             const unsigned char* xb[NT];
 #pragma unroll
             for (int j = 0; j < NT; ++j) xb[j] = x_at[j] + local * (2 * kBlock);
+            bool large = false;  // a zero point of the warp's rows that takes the second subtraction
+            if (P.zeros[0] != nullptr) {
+#pragma unroll
+                for (int w = 0; w < kW; ++w)
+#pragma unroll
+                    for (int i = 0; i < 2 * kGroups; ++i) large |= H::large(zero[w][i / kGroups][i % kGroups]);
+                large = __any_sync(0xffffffffu, large);
+            }
 #pragma unroll
             for (int q = 0; q < kGroups; ++q) {
                 float sum[kW][NT][4];
+                typename H::Zero zeros[kW][2];
+#pragma unroll
+                for (int w = 0; w < kW; ++w)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) zeros[w][h] = H::zero_of(zero[w][h][q]);
 #pragma unroll
                 for (int i = 0; i < STEPS; ++i) {
                     const int step = q * STEPS + i;
@@ -383,8 +422,9 @@ __global__ void __launch_bounds__(32 * kWarps, (Form<NT, GATED, STEPS>::kCtas)) 
 #pragma unroll
                     for (int w = 0; w < kW; ++w) {
                         uint32_t lo[4], hi[4];
-                        widen<T>(*reinterpret_cast<const uint32_t*>(words + w * kTileBytes + 16 * step), mask, sixteen, lo);
-                        widen<T>(*reinterpret_cast<const uint32_t*>(words + w * kTileBytes + 8 * kPitch + 16 * step), mask, sixteen, hi);
+                        H::widen(*reinterpret_cast<const uint32_t*>(words + w * kTileBytes + 16 * step), mask, power, zeros[w][0], large, lo);
+                        H::widen(*reinterpret_cast<const uint32_t*>(words + w * kTileBytes + 8 * kPitch + 16 * step), mask, power, zeros[w][1],
+                                 large, hi);
 #pragma unroll
                         for (int j = 0; j < NT; ++j) {
                             H::mma(sum[w][j], i == 0, lo[0], hi[0], lo[1], hi[1], xv[j].x, xv[j].y);
@@ -392,20 +432,15 @@ __global__ void __launch_bounds__(32 * kWarps, (Form<NT, GATED, STEPS>::kCtas)) 
                         }
                     }
                 }
-                float2 two[NT];  // sums of this lane's two columns of x
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-                    two[j] = *reinterpret_cast<const float2*>(sums_at + (local * kGroups + q) * (4 * F::kXRows) + 32 * j);
 #pragma unroll
                 for (int w = 0; w < kW; ++w) {
                     const float ls = to_f32(scale[w][0][q]), hs = to_f32(scale[w][1][q]);
-                    const float lz = sixteen_and(zero[w][0][q]), hz = sixteen_and(zero[w][1][q]);
 #pragma unroll
                     for (int j = 0; j < NT; ++j) {
-                        acc[w][j][0] = fmaf(ls, fmaf(-lz, two[j].x, sum[w][j][0]), acc[w][j][0]);
-                        acc[w][j][1] = fmaf(ls, fmaf(-lz, two[j].y, sum[w][j][1]), acc[w][j][1]);
-                        acc[w][j][2] = fmaf(hs, fmaf(-hz, two[j].x, sum[w][j][2]), acc[w][j][2]);
-                        acc[w][j][3] = fmaf(hs, fmaf(-hz, two[j].y, sum[w][j][3]), acc[w][j][3]);
+                        acc[w][j][0] = fmaf(ls, sum[w][j][0], acc[w][j][0]);
+                        acc[w][j][1] = fmaf(ls, sum[w][j][1], acc[w][j][1]);
+                        acc[w][j][2] = fmaf(hs, sum[w][j][2], acc[w][j][2]);
+                        acc[w][j][3] = fmaf(hs, sum[w][j][3], acc[w][j][3]);
                     }
                 }
             }
@@ -488,7 +523,7 @@ __global__ void __launch_bounds__(32 * kWarps, (Form<NT, GATED, STEPS>::kCtas)) 
 template <int NT, bool GATED, int STEPS>
 bool plan_smem(W4Params& P, int64_t xrows, int64_t* bytes) {
     using F = Form<NT, GATED, STEPS>;
-    const int64_t per_block = xrows * 2 * F::kBlock + (F::kSteps / P.group_steps) * F::kXRows * 4;
+    const int64_t per_block = xrows * 2 * F::kBlock;
     const int64_t fixed = F::kRingBytes + xrows * 64;
     const int64_t nb = (P.k + F::kBlock - 1) / F::kBlock, mine = std::max<int64_t>(1, (nb + P.split - 1) / P.split);
     const int64_t fits = std::max<int64_t>(1, (F::kSmemMost - fixed) / per_block);

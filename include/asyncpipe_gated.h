@@ -96,9 +96,10 @@ ap_status ap_gated_backward(const void* dy, int64_t lddy, const void* gate, int6
 /*
  * ap_matmul_w4: c = x * W^T for a 4-bit weight W,
  *     c[i, j] = sum over groups of scale * sum over the group's columns of x[i, .] (code - zero);
- * the inner sums are taken of x (16 + code), less 16 + zero times the group's
- * sum of x, all in 32 bits. (An infinity in a row of x, or products that pass the
- * largest float on the way, make that row NaN.)
+ * every sum in 32 bits, of products of x and the whole number code - zero, which are
+ * exact. A column whose code is its zero point takes no part, unless its x is
+ * infinite or NaN, which make that row's result NaN; an infinity times any other
+ * weight is an infinity.
  *  x            m x k of `type` (AP_BF16 or AP_F16), leading dimension ldx.
  *  codes        the weight, n x k as above: 16-byte aligned, ldw (bytes) a
  *               multiple of 16 (AP_ERR_ALIGN otherwise). What a row holds past
