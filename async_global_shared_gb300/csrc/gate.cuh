@@ -32,7 +32,10 @@ inline Gate gate_of(ap_activation act) {
 // there, at -infinity too), and the polynomial takes it up to 128, which keeps
 // infinities out of it; NaN stays NaN. The exponential takes the roundings of its
 // argument, at most three halves of a unit of w, so s is off by at most
-// (8 + 3 |w|) 2^-24 of itself. (gated_grad.cu has the same for two values.)
+// (8 + 3 |w|) 2^-24 of itself while it is a normal number, w above about -87.3. An s
+// below 2^-126 comes out of the reciprocal as 0: act(g) is then 0, off by less than
+// |g| 2^-126 (silu(-88) is -5.3e-37), and its slope 0, off by less than
+// (1 + |g| w'(g)) 2^-126. (gated_grad.cu has the same for two values.)
 __device__ __forceinline__ float min_nan(float a, float b) {
     float r;
     asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));

@@ -11,6 +11,8 @@
  *     AP_ACT_GELU  w = 2 sqrt(2 / pi) (g + 0.044715 g^3), the form with tanh:
  *                  act(g) = g / 2 (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))).
  * act is 0 at minus infinity and infinity at infinity, its slope 0 and 1.
+ * s below 2^-126, w below about -87.3, is taken as 0: act and its slope are 0
+ * there, off by less than |g| 2^-126 and (1 + |g| w'(g)) 2^-126.
  *
  * 4-bit weights. A weight of n rows and k columns is stored row by row, two
  * columns a byte, the even one in the low half, an odd last column in the low
