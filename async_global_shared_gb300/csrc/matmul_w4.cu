@@ -87,13 +87,16 @@ __device__ __forceinline__ uint32_t code_of(uint32_t w, uint32_t mask, uint32_t 
 // x and 16 + code and which takes 16 + zero times the group's sum of x off the group's
 // sum saves that operation, but its sums lose what the correction cancels: a large x
 // where code = zero, all x of one sign, an infinity. It measured 12.6, 20.4 and 63.8 us
-// for the three above: it has to take and keep the sums of x.)
+// for the three above: it has to take and keep the sums of x. In 32 bits c is now off by
+// 3e-8 to 7e-8 of its root mean square, 8 x 2048 x 4096 with x around 0, 1 or 16 standard
+// deviations off it; the plain products in 32 bits by 3e-8 to 4e-7.)
 template <typename T>
 struct Codes;
 template <>
 struct Codes<__nv_bfloat16> {
     // bf16 has every whole number up to 256: of a zero point above 128 the first 128
-    // are taken off with the power, the rest by a second subtraction.
+    // are taken off with the power, the rest by a second subtraction (32 x 8192 x 16384,
+    // zero points of 200: 62.0 us, 59.8 of 8).
     struct Zero {
         uint32_t first, rest;  // 128 + the first, twice; the rest
     };
