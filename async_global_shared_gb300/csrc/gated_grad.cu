@@ -6,9 +6,10 @@
 // and which the forward pass then need not keep.
 //
 // Floor: three inputs read once, each output written once (8192 x 16384 bf16 with
-// all codes, silu: 221 us; it takes 355, 66 % of the issue slots busy with about 70
-// instructions an element; 1237 x 5000 fp16 with all outputs 14 and 34, two rounds of
-// tiles). A block's scale
+// all codes, silu: 221 us; it takes 358, 66 % of the issue slots busy with about 70
+// instructions an element, and at the 128 registers of two CTAs an SM the 16-bit forms
+// spill 60 to 84 bytes a thread; 1237 x 5000 fp16 with all outputs 14 and 34, two rounds
+// of tiles; values alone, 4096 x 16384 bf16, 99 and 98). A block's scale
 // needs its largest magnitude before the first code, and five kinds of codes
 // (dg, du by rows; dg, du, h by columns) of a 128 x 128 tile are more than
 // registers hold, so the tile's inputs stay in shared memory and the three
@@ -64,7 +65,7 @@ __device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
 // product with s = 0):
 //     dg = dy s u (1 + g e s w'(g)),  du = dy s g,  h = g s u.
 // Multiplications and additions take both elements at once (8192 x 16384, all codes:
-// gelu 410 -> 375 us; silu, which has fewer, 354 either way).
+// gelu 410 -> 376 us; silu, which has fewer, the same either way).
 template <bool SILU>
 __device__ __forceinline__ void gradient2(const Gate& p, const float (&dy)[8], const float (&g)[8], const float (&u)[8], int i, float (&dg)[8],
                                           float (&du)[8], float (&h)[8]) {
@@ -229,7 +230,7 @@ struct TileShared {
 // A 128 x 128 tile a CTA: thread t holds rows 8 (t / 16) .. + 7 of columns
 // 8 (t % 16) .. + 7. WHOLE: every row and column exists, and every row starts on
 // a 16-byte boundary (codes: 8). CODES: all codes are asked for and no values, as
-// by a training step (8192 x 16384: 348 us, 379 with the questions left in at the time).
+// by a training step (8192 x 16384, at the time: 348 us, 379 with the questions left in).
 template <typename T, bool SILU, bool WHOLE, bool CODES>
 __device__ __forceinline__ void tile_grad(const GradParams& P, unsigned char* smem_raw, TileShared& sh) {
     using K = Kept<T>;

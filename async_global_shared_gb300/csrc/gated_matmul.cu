@@ -87,10 +87,10 @@ ap_status launch_t(const DeviceInfo& di, int64_t force, const MatmulParams& P, c
     // the SMs' worth of their tiles (256 rows by 128 columns of y) on, else a
     // CTA or cluster a tile of 128 x 128. A CTA by itself loads half again as
     // many bytes a stage, and its tile takes about 4 / 3 of the time of a pair's (2048
-    // x 4096 x 4096: 95 us, 68 in pairs); but where the rows' last 128 would be
-    // empty for a pair it may save a round of tiles (333 x 5000 x 4104: 29 us in one
-    // round, 38 in the pairs' two; 384 x 16384 x 4096, three rounds against four:
-    // 74 and 69).
+    // x 4096 x 4096: 84 us, 68 in pairs; with g, u and e4m3 98 and 72); but where the
+    // rows' last 128 would be empty for a pair it may save a round of tiles (333 x 5000 x
+    // 4104: 27 us in one round, 37 in the pairs' two; 384 x 16384 x 4096, three rounds
+    // against four: 65 and 68 us, with e4m3 72 and 69).
     if (a.m <= 16) return launch_form<C, 16, 1, 5, true>(di, P, G, a, stream);
     if (a.m <= 32) return launch_form<C, 32, 1, 5, true>(di, P, G, a, stream);
     const int64_t pairs = (a.m + 2 * kTile - 1) / (2 * kTile) * ((a.n + kTile - 1) / kTile);

@@ -52,7 +52,7 @@ template <typename C>
 ap_status launch_mm(const DeviceInfo& di, const MatmulParams& P, const MatmulArgs& a, cudaStream_t stream) {
     const bool rows = a.b_block_rows == 1;
     // Few rows: the weight on the accumulator's rows, a's rows padded to 16 or
-    // 32 (times 8192 x 8192: one row 14.5 us, 15.4 padded to 32; 32 rows 16.5,
+    // 32 (times 8192 x 8192: one row 14.2 us, 15.4 padded to 32; 32 rows 16.2,
     // 48 in the 128 x 128 form 18.7).
     if (a.m <= 16) return launch_form<C, 16, 1, 4, true, true>(di, P, a, stream);
     if (a.m <= 32) return launch_form<C, 32, 1, 4, true, true>(di, P, a, stream);

@@ -23,9 +23,9 @@
 // sums its share, and the shares are added through distributed shared memory
 // in rank order.
 //
-// What bounds it. One token times 8192 x 8192: the weight's bytes, 14.5 us = 4.6
-// TB/s, of which 5 are the launch, the first loads and the reduction (8 tokens
-// times 28672 x 8192: 40.5 us = 5.8 TB/s). 128 x 128 tiles: the consumers'
+// What bounds it. One token times 8192 x 8192: the weight's bytes, 14.2 to 14.5
+// us = 4.7 TB/s, of which 5 are the launch, the first loads and the reduction (8
+// tokens times 28672 x 8192: 39.5 to 40.5 us = 5.9 TB/s). 128 x 128 tiles: the consumers'
 // instructions, 66 % of the issue slots over a CTA's life, beside 512 cycles a
 // block of shared memory, 59 % (333 x 4104 x 5000: 18.6 us, a quarter of it
 // launch, first loads and exit). 8192^3 in pairs: 440 us = 2.5

@@ -14,11 +14,13 @@
 //    and i + 4 at once into a pair of 16-bit numbers code - zero (see Codes).
 //  - The products run on the warp's matrix instruction m16n8k16 with the
 //    weight's rows on its 16 rows and the rows of x on its 8 columns, so up to
-//    8 rows of x cost what one costs. (tcgen05 would want the widened codes
-//    back in shared memory, four times the bytes that arrive.) Columns may be
-//    taken in any order as long as both operands agree: x is staged with every
-//    eight of its values in the order 0 4 1 5 2 6 3 7, which is how the codes
-//    come out of a word.
+//    8 rows of x cost what one costs. (The tensor memory's instructions take the
+//    weight from tensor memory or shared memory, so the widened codes, four times the
+//    bytes that arrive, would be written there first. For 8 rows of x that is more
+//    work; for many, whose weight would be widened once, it would be less: not built.)
+//    Columns may be taken in any order as long as both operands agree: x is staged
+//    with every eight of its values in the order 0 4 1 5 2 6 3 7, which is how the
+//    codes come out of a word.
 //  - A group's products are summed by themselves and then scaled, in 32 bits.
 //  - x is staged for a stretch of blocks at a time.
 //  - The warps of a CTA share the staged x. Where that leaves few CTAs a cluster
@@ -26,10 +28,11 @@
 //    order.
 // It measured (the codes at the rate of a copy would take 5.1, 10.2 and 11 us): one row
 // times 8192 x 8192 13.0 us, gated times 16384 x 4096 20.9, 32 rows times 8192 x 16384
-// 59.7. What bounds it then are instructions, half of them the widening (11 for a word's
-// eight codes in bf16, 9 in fp16), and a thousand a warp around them; with two CTAs of
-// eight warps an SM the issue slots are about half busy, and waits on the ring, the
-// matrix instructions and one another take the rest.
+// 59.7. What bounds it then are instructions, 385 for 256 columns of 16 rows with all that
+// is around them (the first case), about 176 of them the widening (11 for a word's eight
+// codes; 9 in fp16); with two CTAs of eight warps an SM the issue slots are 43 % busy, and
+// waits on the ring, the matrix instructions and one another take the rest. More than 32
+// rows: 8192 x 8192 times 128 rows 89 us, 2048 rows 1220, 193 and 225 TFLOP/s.
 #include <algorithm>
 #include <atomic>
 
@@ -545,7 +548,7 @@ ap_status launch_form(const DeviceInfo& di, W4Params P, cudaStream_t stream) {
     const int64_t xrows = std::min<int64_t>(P.m, F::kXRows);
     // Warps with rows of their own: all eight, which share the staged x, unless k in
     // eight shares then leaves SMs without a CTA; and k in so many shares as keep
-    // all CTAs resident, each with two steps of the ring at least. (1 x 4096 x
+    // all CTAs resident, each with two steps of the ring at least. (At the time: 1 x 4096 x
     // 16384: one and all of k a CTA 15.6 us, eight and an eighth 12.8; 1 x 8192 x
     // 8192: two 13.3, eight and a quarter 12.8; 32 x 8192 x 16384: four and a half
     // 81, eight and a quarter 64; the other way 1 x 1024 x 4096: eight 4.5, two 3.9.)
