@@ -101,7 +101,8 @@ ap_status ap_gated_backward(const void* dy, int64_t lddy, const void* gate, int6
  * every sum in 32 bits, of products of x and the whole number code - zero, which are
  * exact. A column whose code is its zero point takes no part, unless its x is
  * infinite or NaN, which make that row's result NaN; an infinity times any other
- * weight is an infinity.
+ * weight is an infinity. (So is a group's sum that passes the largest float before
+ * its scale.)
  *  x            m x k of `type` (AP_BF16 or AP_F16), leading dimension ldx.
  *  codes        the weight, n x k as above: 16-byte aligned, ldw (bytes) a
  *               multiple of 16 (AP_ERR_ALIGN otherwise). What a row holds past
